@@ -272,6 +272,116 @@ stq_status stq_allocate_widths(int32_t num_heads, int32_t d, const double *disto
 stq_status stq_row_impact(int32_t T, int32_t H, int32_t d, int32_t gate, int32_t in_dtype, const void *q,
                           const void *k, const float *beta, const float *alpha, float *w_out, void *stream);
 
+/* ------------------------------------------------------------------------------------------
+ * The layers next to the quantized ones. A hybrid stack mixes delta-rule layers, whose state the
+ * calls above keep as codes, with linear-attention layers whose heads only decay and with softmax
+ * attention over a key-value cache (the models the pages serve are hybrids of this kind: "K1
+ * 論文詳解", section 方法). The calls below serve those layers under the same conventions. The pages
+ * give no formula for them; these are the definitions:
+ *
+ *   decay     S <- alpha S + k v^T ;  o = S^T q          (S: d x d fp32, readout after the update)
+ *   attention o = sum_t softmax_t(scale q.k_t) v_t       (t: the cached tokens of the request)
+ *
+ * Every accumulation, softmax statistic and state is fp32; o is fp32 for both input types.
+ * ------------------------------------------------------------------------------------------ */
+
+/* One token of decayed linear attention, in place, for B requests of H heads.
+ *   states      device fp32 [state_slots][H][d][d], 16-byte aligned: the state pool
+ *   slots       device int32 [B], the pool slot of each request (distinct); a request whose slot is
+ *               out of range is skipped and flagged
+ *   q, k, v     device [B][H][d] of in_dtype, 16-byte aligned
+ *   alpha       device fp32 [B][H], the token's decay of each head (any finite value; 0 clears)
+ *   o           device fp32 [B][H][d], 16-byte aligned, written
+ * d in {16, 32, 64, 128}. A state slot has the layout stq_init_state takes and stq_dequantize gives
+ * (fp32 [H][d][d]), so an idle request's state can be parked as codes. B == 0 is a no-op. */
+stq_status stq_decay_step(int32_t B, int32_t H, int32_t d, int32_t in_dtype, float *states, int32_t state_slots,
+                          const int32_t *slots, const void *q, const void *k, const void *v, const float *alpha,
+                          float *o, int32_t *dev_status, void *stream);
+
+/* Workspace bytes stq_decay_prefill can use (0: it uses none for this shape). */
+size_t stq_decay_prefill_workspace_bytes(int32_t B, int32_t H, int32_t T, int32_t d, int32_t in_dtype);
+
+/* The same recurrence over prompts: token t of request b is the decay step on (q, k, v, alpha) at t.
+ *   q, k, v     device [B][H][T][d] of in_dtype, 16-byte aligned
+ *   alpha       device fp32 [B][H][T]
+ *   lens        device int32 [B], tokens of each prompt, or NULL: T for all. Tokens behind a prompt's
+ *               end change nothing: their rows of q, k, v and alpha are not used (NaN may stand
+ *               there) and their rows of o stay as they were. A length outside [0, T] skips the
+ *               request and is flagged.
+ *   o           device fp32 [B][H][T][d], 16-byte aligned, written
+ *   workspace   device scratch of >= stq_decay_prefill_workspace_bytes(...) bytes, 256-byte aligned,
+ *               or NULL (slower where the size is not 0). A workspace that is given but too small or
+ *               misaligned is STQ_ERR_INVALID_ARG; calls in flight at the same time need separate
+ *               workspaces.
+ * B == 0 or T == 0 is a no-op. */
+stq_status stq_decay_prefill(int32_t B, int32_t H, int32_t T, int32_t d, int32_t in_dtype, float *states,
+                             int32_t state_slots, const int32_t *slots, const void *q, const void *k, const void *v,
+                             const float *alpha, const int32_t *lens, float *o, void *workspace,
+                             size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* The paged cache. Keys and values live in pages [num_pages][kv_heads][page_size][d]; request b's
+ * token at position t is row t % page_size of page table[b][t / page_size]. A slot is
+ * page * page_size + row.
+ *
+ * stq_page_plan gives the new tokens of a step their pages and slots, on the device: request b holds
+ * lens[b] tokens, gets fresh[b] more, and takes the pages it lacks from the free list, in request
+ * order.
+ *   table       device int32 [B][table_width]; the entries of newly taken pages are written
+ *   lens, fresh device int32 [B]
+ *   free_pages  device int32 [num_free], page indices; those before *free_head are taken
+ *   free_head   device int32 [1]
+ *   slot_map    device int32 [slot_map_size], written: the slots of the new tokens, request after
+ *               request, then -1 to the end
+ *   starts      device int32 [B + 1], written: where each request's tokens start in slot_map
+ *   lens_out    device int32 [B], written: lens + fresh;  may be lens itself
+ *   head_out    device int32 [1], written: the list's new head;  may be free_head itself
+ * All or nothing per request: one with a negative count, with more tokens than its table row spans,
+ * for whose pages the list (taken in order) is too short, or whose tokens pass the slot map's end gets no
+ * pages; its length and table row stay, its tokens' slots are -1, and STQ_ERR_BOUNDS is flagged. A
+ * request that needs no new page is served whatever the list holds. Slots must be int32: a page
+ * whose slots are not (or a negative page) gives -1 and is flagged. */
+stq_status stq_page_plan(int32_t B, int32_t table_width, int32_t page_size, int32_t *table, const int32_t *lens,
+                         const int32_t *fresh, const int32_t *free_pages, int32_t num_free, const int32_t *free_head,
+                         int32_t *slot_map, int32_t slot_map_size, int32_t *starts, int32_t *lens_out,
+                         int32_t *head_out, int32_t *dev_status, void *stream);
+
+/* Write N new tokens' keys and values to their slots.
+ *   k_pages, v_pages  device [num_pages][kv_heads][page_size][d] of dtype, 16-byte aligned
+ *   slot_map    device int32 [N]; -1 skips the token, any other slot outside the pages skips it and
+ *               is flagged. Slots >= 0 must be distinct.
+ *   k, v        device [N][kv_heads][d] of dtype, 16-byte aligned; consecutive tokens k_stride and
+ *               v_stride elements apart (>= kv_heads * d, a multiple of 16 bytes), so that both may
+ *               be parts of one projection's rows
+ * d in {16, 32, 64, 128}. N == 0 is a no-op. */
+stq_status stq_page_write(int32_t N, int32_t kv_heads, int32_t d, int32_t dtype, int32_t page_size, int32_t num_pages,
+                          void *k_pages, void *v_pages, const int32_t *slot_map, const void *k, const void *v,
+                          int64_t k_stride, int64_t v_stride, int32_t *dev_status, void *stream);
+
+/* Workspace bytes for stq_paged_attention (any lengths, pages and table width). Host only. */
+size_t stq_paged_attention_workspace_bytes(int32_t B, int32_t q_heads, int32_t d, int32_t kv_heads);
+
+/* Attention of one new token per request over the paged cache; query head h reads key-value head
+ * h / (q_heads / kv_heads).
+ *   q           device [B][q_heads][d] of dtype, 16-byte aligned
+ *   table       device int32 [B][table_width]; entries behind a request's last page are not read
+ *   lens        device int32 [B], cached tokens (the new one included). 0 (a padded row) gives o = 0;
+ *               a length outside [0, table_width * page_size] does too, and is flagged
+ *   scale       finite
+ *   o           device fp32 [B][q_heads][d], 16-byte aligned, written
+ *   workspace   device scratch of >= stq_paged_attention_workspace_bytes(...) bytes, 256-byte
+ *               aligned, or NULL. With it the cached tokens of all requests are split evenly over
+ *               the GPU and the parts joined; without it one thread block reads a key-value head's
+ *               whole cache (slower for few or long requests). Given but too small or misaligned:
+ *               STQ_ERR_INVALID_ARG. Calls in flight at the same time need separate workspaces.
+ * Rows of a page behind a request's last token are not used (NaN may stand there). Tokens on a page
+ * outside [0, num_pages) are left out and flagged. A row whose scores are all -inf gives o = 0.
+ * d in {16, 32, 64, 128}. B == 0 is a no-op. */
+stq_status stq_paged_attention(int32_t B, int32_t q_heads, int32_t kv_heads, int32_t d, int32_t dtype,
+                               int32_t page_size, int32_t num_pages, int32_t table_width, const void *q,
+                               const void *k_pages, const void *v_pages, const int32_t *table, const int32_t *lens,
+                               float scale, float *o, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                               void *stream);
+
 /* Self-test of the bounded wait every kernel of this library uses on its copies: one CTA waits on
  * a barrier that nothing completes, gives up after the library's cap (about 4e9 SM clock cycles,
  * ~2 s), ORs the STQ_ERR_TIMEOUT bit into *dev_status and exits, leaving the context usable. It

@@ -29,7 +29,8 @@ EXPORTS = (
     "stq_layout_bytes_per_request", "stq_layout_head_offset", "stq_layout_head_bytes",
     "stq_layout_head_bits", "stq_init_state", "stq_decode_step", "stq_prefill_workspace_bytes",
     "stq_prefill_chunk", "stq_prefill_chunk_noalloc", "stq_dequantize", "stq_allocate_widths", "stq_row_impact",
-    "stq_selftest_wait_timeout",
+    "stq_selftest_wait_timeout", "stq_decay_step", "stq_decay_prefill_workspace_bytes", "stq_decay_prefill",
+    "stq_page_plan", "stq_page_write", "stq_paged_attention_workspace_bytes", "stq_paged_attention",
 )
 
 
@@ -86,6 +87,22 @@ def lib() -> ctypes.CDLL:
             L.stq_row_impact.argtypes = [i32, i32, i32, i32, i32, P, P, P, P, P, P]
             L.stq_row_impact.restype = i32
             L.stq_selftest_wait_timeout.argtypes, L.stq_selftest_wait_timeout.restype = [P, P], i32
+            i64 = ctypes.c_int64
+            L.stq_decay_step.argtypes = [i32, i32, i32, i32, P, i32, P, P, P, P, P, P, P, P]
+            L.stq_decay_step.restype = i32
+            L.stq_decay_prefill_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+            L.stq_decay_prefill_workspace_bytes.restype = sz
+            L.stq_decay_prefill.argtypes = [i32, i32, i32, i32, i32, P, i32, P, P, P, P, P, P, P, P, sz, P, P]
+            L.stq_decay_prefill.restype = i32
+            L.stq_page_plan.argtypes = [i32, i32, i32, P, P, P, P, i32, P, P, i32, P, P, P, P, P]
+            L.stq_page_plan.restype = i32
+            L.stq_page_write.argtypes = [i32, i32, i32, i32, i32, i32, P, P, P, P, P, i64, i64, P, P]
+            L.stq_page_write.restype = i32
+            L.stq_paged_attention_workspace_bytes.argtypes = [i32, i32, i32, i32]
+            L.stq_paged_attention_workspace_bytes.restype = sz
+            L.stq_paged_attention.argtypes = [i32, i32, i32, i32, i32, i32, i32, i32, P, P, P, P, P, ctypes.c_float,
+                                              P, P, sz, P, P]
+            L.stq_paged_attention.restype = i32
             _lib_handle = L
     return _lib_handle
 
@@ -311,3 +328,175 @@ def row_impact(q, k, beta, alpha, gate: int = GATE_SCALAR, stream=None) -> torch
     _check(lib().stq_row_impact(T, H, d, int(gate), _DTYPES[q.dtype], _ptr(q), _ptr(k), _ptr(beta), _ptr(alpha),
                                 _ptr(w), _stream(stream)), "stq_row_impact")
     return w
+
+
+# --------------------------------------------------------------------------------------------
+# The layers next to the quantized ones: decayed linear attention, paged cache and attention.
+# These calls run on the device of their tensors, whatever the current one is.
+# --------------------------------------------------------------------------------------------
+def _call(fn, what: str, dev: torch.device, status, stream, *args):
+    """fn(*args, status, stream) with `dev` current and its current stream where none is given."""
+    if dev.type != "cuda":
+        raise ValueError(f"{what}: tensors are on {dev}, expected a CUDA device")
+    if status is not None:
+        _need(status, "status", torch.int32, (1,), dev)
+    here = torch.cuda.current_device()
+    if dev.index is None or dev.index == here:
+        st = fn(*args, None if status is None else status.data_ptr(), _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, None if status is None else status.data_ptr(), _stream(stream))
+    if st != STQ_OK:
+        raise StqError(st, what)
+
+
+def _workspace(workspace, need: int, dev):
+    """(pointer, bytes) of a workspace argument; a call that needs none ignores what it is given."""
+    if workspace is None or not need:
+        return None, 0
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {dev}")
+    n = workspace.numel() * workspace.element_size()
+    if n < need:
+        raise ValueError(f"workspace of {n} bytes is below the {need} bytes it needs")
+    return workspace.data_ptr(), n
+
+
+def _dtype(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected float32 or bfloat16")
+    return code
+
+
+def _decay_args(states, slots, q, k, v, alpha, o):
+    code, shape, dev = _dtype(q, "q"), q.shape, q.device
+    B, H, d = shape[0], shape[1], shape[-1]
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _need(t, name, q.dtype, shape, dev)
+    if not isinstance(states, torch.Tensor) or states.dim() != 4:
+        raise ValueError("states must be a [slots, heads, d, d] tensor")
+    _need(states, "states", torch.float32, (states.shape[0], H, d, d), dev)
+    _need(slots, "slots", torch.int32, (B,), dev)
+    _need(alpha, "alpha", torch.float32, shape[:-1], dev)
+    _need(o, "o", torch.float32, shape, dev)
+    return code, dev
+
+
+def decay_step(states, slots, q, k, v, alpha, o, status=None, stream=None):
+    """One token of linear attention with a decay per head, in place: S <- alpha S + k v^T, o = S^T q.
+
+    states [slots, H, d, d] fp32, slots [B] int32, q, k, v [B, H, d] (float32 or bfloat16), alpha
+    [B, H] fp32, o [B, H, d] fp32. See stq_decay_step in include/stq.h."""
+    if isinstance(q, torch.Tensor) and q.dim() != 3:
+        raise ValueError("q must be [B, H, d]")
+    code, dev = _decay_args(states, slots, q, k, v, alpha, o)
+    B, H, d = q.shape
+    _call(lib().stq_decay_step, "stq_decay_step", dev, status, stream, B, H, d, code, states.data_ptr(),
+          states.shape[0], slots.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), alpha.data_ptr(), o.data_ptr())
+
+
+def decay_prefill_workspace_bytes(B: int, H: int, T: int, d: int, in_dtype: torch.dtype) -> int:
+    """Workspace bytes decay_prefill can use (0: none for this shape)."""
+    if in_dtype not in _DTYPES:
+        raise TypeError(f"unsupported input dtype {in_dtype}")
+    return lib().stq_decay_prefill_workspace_bytes(B, H, T, d, _DTYPES[in_dtype])
+
+
+def decay_prefill(states, slots, q, k, v, alpha, o, lens=None, workspace=None, status=None, stream=None):
+    """decay_step over prompts: q, k, v [B, H, T, d], alpha [B, H, T], o [B, H, T, d] fp32, lens [B]
+    int32 (tokens of each prompt; rows behind them are left alone) or None for T. See
+    stq_decay_prefill in include/stq.h."""
+    if isinstance(q, torch.Tensor) and q.dim() != 4:
+        raise ValueError("q must be [B, H, T, d]")
+    code, dev = _decay_args(states, slots, q, k, v, alpha, o)
+    B, H, T, d = q.shape
+    if lens is not None:
+        _need(lens, "lens", torch.int32, (B,), dev)
+    ws, ws_bytes = _workspace(workspace, lib().stq_decay_prefill_workspace_bytes(B, H, T, d, code), dev)
+    _call(lib().stq_decay_prefill, "stq_decay_prefill", dev, status, stream, B, H, T, d, code, states.data_ptr(),
+          states.shape[0], slots.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), alpha.data_ptr(),
+          None if lens is None else lens.data_ptr(), o.data_ptr(), ws, ws_bytes)
+
+
+def page_plan(table, lens, fresh, free_pages, free_head, slot_map, starts, lens_out, head_out, page_size: int,
+              status=None, stream=None):
+    """Pages, table entries and slots of the fresh[b] new tokens of requests that hold lens[b], from
+    the free list (all int32 tensors; lens_out and head_out may be lens and free_head themselves).
+    See stq_page_plan in include/stq.h."""
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table must be a [B, width] tensor")
+    dev, (B, W) = table.device, table.shape
+    _need(table, "table", torch.int32, (B, W), dev)
+    for name, t, n in (("lens", lens, B), ("fresh", fresh, B), ("free_pages", free_pages, None),
+                       ("free_head", free_head, 1), ("slot_map", slot_map, None), ("starts", starts, B + 1),
+                       ("lens_out", lens_out, B), ("head_out", head_out, 1)):
+        if n is None:
+            if not isinstance(t, torch.Tensor) or t.dim() != 1:
+                raise ValueError(f"{name} must be a 1-D tensor")
+            n = t.shape[0]
+        _need(t, name, torch.int32, (n,), dev)
+    _call(lib().stq_page_plan, "stq_page_plan", dev, status, stream, B, W, int(page_size), table.data_ptr(),
+          lens.data_ptr(), fresh.data_ptr(), free_pages.data_ptr(), free_pages.shape[0], free_head.data_ptr(),
+          slot_map.data_ptr(), slot_map.shape[0], starts.data_ptr(), lens_out.data_ptr(), head_out.data_ptr())
+
+
+def _pages(k_pages, v_pages, kind, Hkv, d, dev):
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        raise ValueError("k_pages must be a [pages, kv_heads, page_size, d] tensor")
+    n, heads, page, _ = k_pages.shape
+    shape = (n, heads if Hkv is None else Hkv, page, d)
+    _need(k_pages, "k_pages", kind, shape, dev)
+    _need(v_pages, "v_pages", kind, shape, dev)
+    return shape
+
+
+def page_write(k_pages, v_pages, slot_map, k, v, status=None, stream=None):
+    """Write new tokens' keys and values [N, kv_heads, d] to their slots of the paged cache
+    [pages, kv_heads, page_size, d]; slot -1 skips a token. k and v may be strided over tokens. See
+    stq_page_write in include/stq.h."""
+    code = _dtype(k, "k")
+    if k.dim() != 3:
+        raise ValueError("k must be [N, kv_heads, d]")
+    (N, Hkv, d), dev = k.shape, k.device
+    n, _, page, _ = _pages(k_pages, v_pages, k.dtype, Hkv, d, dev)
+    _need(slot_map, "slot_map", torch.int32, (N,), dev)
+    strides = []
+    for name, t in (("k", k), ("v", v)):
+        if not isinstance(t, torch.Tensor) or t.dtype != k.dtype or t.device != dev or t.shape != k.shape:
+            raise ValueError(f"{name} must be a {k.dtype} tensor of shape {tuple(k.shape)} on {dev}")
+        row, head, unit = t.stride()
+        if (unit != 1 and d > 1) or (head != d and Hkv > 1) or (row < Hkv * d and N > 1):
+            raise ValueError(f"{name}: a token's heads must be contiguous and tokens must not overlap")
+        strides.append(row if N > 1 else Hkv * d)
+    _call(lib().stq_page_write, "stq_page_write", dev, status, stream, N, Hkv, d, code, page, n, k_pages.data_ptr(),
+          v_pages.data_ptr(), slot_map.data_ptr(), k.data_ptr(), v.data_ptr(), *strides)
+
+
+def paged_attention_workspace_bytes(B: int, q_heads: int, d: int, kv_heads: int) -> int:
+    """Workspace bytes of paged_attention."""
+    return lib().stq_paged_attention_workspace_bytes(B, q_heads, d, kv_heads)
+
+
+def paged_attention(q, k_pages, v_pages, table, lens, o, scale: float, workspace=None, status=None, stream=None):
+    """Attention of one new token per request, q [B, q_heads, d], over the lens[b] cached tokens of
+    its table row; o [B, q_heads, d] fp32. With a workspace the cache is split over the GPU. See
+    stq_paged_attention in include/stq.h."""
+    code = _dtype(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [B, q_heads, d]")
+    (B, Hq, d), dev = q.shape, q.device
+    _need(q, "q", q.dtype, (B, Hq, d), dev)
+    n, Hkv, page, _ = _pages(k_pages, v_pages, q.dtype, None, d, dev)
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table must be a [B, width] tensor")
+    W = table.shape[1]
+    _need(table, "table", torch.int32, (B, W), dev)
+    _need(lens, "lens", torch.int32, (B,), dev)
+    _need(o, "o", torch.float32, (B, Hq, d), dev)
+    ws, ws_bytes = _workspace(workspace, lib().stq_paged_attention_workspace_bytes(B, Hq, d, Hkv), dev)
+    _call(lib().stq_paged_attention, "stq_paged_attention", dev, status, stream, B, Hq, Hkv, d, code, page, n, W,
+          q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), lens.data_ptr(), float(scale),
+          o.data_ptr(), ws, ws_bytes)

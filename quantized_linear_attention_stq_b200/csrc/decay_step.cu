@@ -1,0 +1,312 @@
+// decay_step.cu -- linear attention with a decay per head, without the delta term, on an fp32 state
+// pool (contract in include/stq.h): one token (stq_decay_step) and the token-by-token prompt form.
+//
+//   S <- alpha S + k v^T ;  o = S^T q      (readout after the update)
+//
+// One token. Bound by HBM: a head's state is read and written once (8 d^2 bytes), with 5 d^2
+// operations. One CTA per (request, head) keeps the whole state in registers between its load and
+// its store, all loads of a thread in flight at once; a warp's lanes hold consecutive columns, so
+// rows move in whole 128-byte lines and the readout is a sum over the CTA's row groups.
+//
+// Token by token. The state of a block of columns stays in registers for the whole prompt (columns
+// of S are independent of each other); tokens are staged through shared memory 32 at a time. A
+// column's rows are spread over SL lanes, joined by shuffles per token.
+#include "../../include/stq.h"
+#include "stq_decay.cuh"
+
+namespace stq {
+namespace {
+
+template <int IN_BF16>
+__device__ __forceinline__ float4 load_in4(const void *base, size_t idx)
+{
+    if constexpr (IN_BF16) {
+        const uint2 r = *reinterpret_cast<const uint2 *>(reinterpret_cast<const __nv_bfloat16 *>(base) + idx);
+        return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u), __uint_as_float(r.y << 16),
+                           __uint_as_float(r.y & 0xFFFF0000u));
+    } else {
+        return *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(base) + idx);
+    }
+}
+
+template <int D>
+struct StepCfg {
+    static constexpr int C4 = D / 4;                                  // float4 columns of a row
+    static constexpr int NT = D * C4 < 256 ? D * C4 : 256;            // threads
+    static constexpr int RG = NT / C4;                                // rows of one pass
+    static constexpr int NR = D / RG;                                 // passes
+};
+
+template <int D, int IN_BF16>
+__global__ void __launch_bounds__(StepCfg<D>::NT) decay_step_kernel(const DecayParams p)
+{
+    using S = StepCfg<D>;
+    __shared__ float4 part[S::RG][S::C4];
+    __shared__ float qs[D], ks[D];
+    const int tid = threadIdx.x, c = tid % S::C4, rg = tid / S::C4;
+    const size_t tile = blockIdx.x;  // (request, head)
+    const int b = (int)(tile / (unsigned)p.H), h = (int)(tile - (size_t)b * p.H);
+    const int slot = p.slots[b];
+    if (slot < 0 || slot >= p.state_slots) {
+        if (tid == 0) flag(p.status, kFlagBounds);
+        return;
+    }
+    float4 *st = reinterpret_cast<float4 *>(p.states + ((size_t)slot * p.H + h) * (D * D)) + (size_t)rg * S::C4 + c;
+    float4 s[S::NR];
+#pragma unroll
+    for (int i = 0; i < S::NR; ++i) s[i] = __ldcs(st + (size_t)i * S::RG * S::C4);
+    for (int i = tid; i < D; i += S::NT) {
+        qs[i] = load_in<IN_BF16>(p.q, tile * D + i);
+        ks[i] = load_in<IN_BF16>(p.k, tile * D + i);
+    }
+    const float4 v = load_in4<IN_BF16>(p.v, tile * D + 4 * c);
+    const float a = p.alpha[tile];
+    __syncthreads();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < S::NR; ++i) {
+        const int row = rg + i * S::RG;
+        const float kk = ks[row], qq = qs[row];
+        s[i].x = fmaf(a, s[i].x, kk * v.x);
+        s[i].y = fmaf(a, s[i].y, kk * v.y);
+        s[i].z = fmaf(a, s[i].z, kk * v.z);
+        s[i].w = fmaf(a, s[i].w, kk * v.w);
+        __stcs(st + (size_t)i * S::RG * S::C4, s[i]);
+        acc.x = fmaf(qq, s[i].x, acc.x);
+        acc.y = fmaf(qq, s[i].y, acc.y);
+        acc.z = fmaf(qq, s[i].z, acc.z);
+        acc.w = fmaf(qq, s[i].w, acc.w);
+    }
+    // a state entry that is not finite may meet a zero query entry: 0 * it is NaN, so it is tested here
+    float bad = 0.f;
+#pragma unroll
+    for (int i = 0; i < S::NR; ++i)
+        bad += (s[i].x - s[i].x) + (s[i].y - s[i].y) + (s[i].z - s[i].z) + (s[i].w - s[i].w);
+    part[rg][c] = acc;
+    __syncthreads();
+    if (tid < S::C4) {
+        float4 t = part[0][c];
+#pragma unroll
+        for (int r = 1; r < S::RG; ++r) {
+            const float4 x = part[r][c];
+            t.x += x.x;
+            t.y += x.y;
+            t.z += x.z;
+            t.w += x.w;
+        }
+        bad += (t.x - t.x) + (t.y - t.y) + (t.z - t.z) + (t.w - t.w);
+        *reinterpret_cast<float4 *>(p.o + tile * D + 4 * c) = t;
+    }
+    if (bad != 0.f) flag(p.status, kFlagNonfinite);  // x - x is 0 for a finite x, NaN otherwise
+}
+
+template <int D>
+struct SerialCfg {
+    static constexpr int SL = D >= 32 ? 8 : 4;          // lanes sharing a column
+    static constexpr int RW = D / SL;                   // rows of a lane
+    static constexpr int CB = D < 32 ? D : 32;          // columns of a CTA
+    static constexpr int NT = CB * SL;
+    static constexpr int TB = 32;                       // tokens staged at a time
+};
+
+template <int D, int IN_BF16>
+__global__ void __launch_bounds__(SerialCfg<D>::NT) decay_serial_kernel(const DecayParams p)
+{
+    using S = SerialCfg<D>;
+    __shared__ __align__(16) float qs[S::TB][D], ks[S::TB][D];
+    __shared__ float vs[S::TB][S::CB], os[S::TB][S::CB], as[S::TB];
+    const int tid = threadIdx.x, r = tid % S::SL, cl = tid / S::SL;
+    const int c0 = blockIdx.x * S::CB;
+    const size_t tile = blockIdx.y + (size_t)blockIdx.z * gridDim.y;  // (request, head)
+    if (tile >= (size_t)p.B * p.H) return;
+    const int b = (int)(tile / (unsigned)p.H), h = (int)(tile - (size_t)b * p.H);
+    const int slot = p.slots[b];
+    const int len = prompt_length(p, b);
+    if (slot < 0 || slot >= p.state_slots || len < 0) {
+        if (tid == 0) flag(p.status, kFlagBounds);
+        return;
+    }
+    if (len == 0) return;
+    float *st = p.states + ((size_t)slot * p.H + h) * (D * D) + c0 + cl;
+    // rows of a lane: groups of 4, SL groups apart, so that the lanes' 16-byte reads of k and q are adjacent
+    float s[S::RW];
+#pragma unroll
+    for (int i = 0; i < S::RW; ++i) s[i] = st[(size_t)((i / 4 * S::SL + r) * 4 + i % 4) * D];
+    const size_t base = tile * (size_t)p.T;
+    for (int t0 = 0; t0 < len; t0 += S::TB) {
+        const int n = len - t0 < S::TB ? len - t0 : S::TB;
+        for (int i = tid; i < n * D; i += S::NT) {
+            (&qs[0][0])[i] = load_in<IN_BF16>(p.q, (base + t0) * D + i);
+            (&ks[0][0])[i] = load_in<IN_BF16>(p.k, (base + t0) * D + i);
+        }
+        for (int i = tid; i < n * S::CB; i += S::NT)
+            vs[i / S::CB][i % S::CB] = load_in<IN_BF16>(p.v, (base + t0 + i / S::CB) * D + c0 + i % S::CB);
+        for (int i = tid; i < n; i += S::NT) as[i] = p.alpha[base + t0 + i];
+        __syncthreads();
+#pragma unroll 4
+        for (int t = 0; t < n; ++t) {
+            const float a = as[t], v = vs[t][cl];
+            float acc = 0.f;
+#pragma unroll
+            for (int i = 0; i < S::RW; i += 4) {
+                const float4 k4 = *reinterpret_cast<const float4 *>(&ks[t][(i / 4 * S::SL + r) * 4]);
+                const float4 q4 = *reinterpret_cast<const float4 *>(&qs[t][(i / 4 * S::SL + r) * 4]);
+                s[i] = fmaf(a, s[i], k4.x * v);
+                s[i + 1] = fmaf(a, s[i + 1], k4.y * v);
+                s[i + 2] = fmaf(a, s[i + 2], k4.z * v);
+                s[i + 3] = fmaf(a, s[i + 3], k4.w * v);
+                acc = fmaf(q4.x, s[i], acc);
+                acc = fmaf(q4.y, s[i + 1], acc);
+                acc = fmaf(q4.z, s[i + 2], acc);
+                acc = fmaf(q4.w, s[i + 3], acc);
+            }
+#pragma unroll
+            for (int m = S::SL / 2; m > 0; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
+            if (r == 0) os[t][cl] = acc;
+        }
+        __syncthreads();
+        float bad = 0.f;
+        for (int i = tid; i < n * S::CB; i += S::NT) {
+            const float x = os[i / S::CB][i % S::CB];
+            bad += x - x;
+            p.o[(base + t0 + i / S::CB) * D + c0 + i % S::CB] = x;
+        }
+        if (bad != 0.f) flag(p.status, kFlagNonfinite);
+        // os is next written behind the next block's staging barrier, so no third barrier is needed
+    }
+    float bad = 0.f;
+#pragma unroll
+    for (int i = 0; i < S::RW; ++i) {
+        st[(size_t)((i / 4 * S::SL + r) * 4 + i % 4) * D] = s[i];
+        bad += s[i] - s[i];
+    }
+    if (bad != 0.f) flag(p.status, kFlagNonfinite);
+}
+
+template <int D>
+cudaError_t step(const DecayParams &p, int in_bf16, cudaStream_t s)
+{
+    const unsigned grid = (unsigned)((size_t)p.B * p.H);
+    if (in_bf16)
+        decay_step_kernel<D, 1><<<grid, StepCfg<D>::NT, 0, s>>>(p);
+    else
+        decay_step_kernel<D, 0><<<grid, StepCfg<D>::NT, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t serial(const DecayParams &p, int in_bf16, cudaStream_t s)
+{
+    const size_t tiles = (size_t)p.B * p.H;
+    const unsigned gy = (unsigned)(tiles < 32768 ? tiles : 32768);
+    const dim3 grid(D / SerialCfg<D>::CB, gy, (unsigned)((tiles + gy - 1) / gy));
+    if (in_bf16)
+        decay_serial_kernel<D, 1><<<grid, SerialCfg<D>::NT, 0, s>>>(p);
+    else
+        decay_serial_kernel<D, 0><<<grid, SerialCfg<D>::NT, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_decay_serial(const DecayParams &p, int d, int in_bf16, cudaStream_t s)
+{
+    switch (d) {
+        case 16: return serial<16>(p, in_bf16, s);
+        case 32: return serial<32>(p, in_bf16, s);
+        case 64: return serial<64>(p, in_bf16, s);
+        default: return serial<128>(p, in_bf16, s);
+    }
+}
+
+}  // namespace stq
+
+namespace {
+
+bool decay_aligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) % 16) == 0; }
+
+// Arguments that both forms share; `work` is false for a call without any.
+stq_status check_decay(int32_t B, int32_t H, int32_t T, int32_t d, int32_t in_dtype, const float *states,
+                       int32_t state_slots, const int32_t *slots, const void *q, const void *k, const void *v,
+                       const float *alpha, const float *o, bool *work)
+{
+    *work = false;
+    if (B < 0 || H < 1 || T < 0 || state_slots < 0 || (in_dtype != STQ_F32 && in_dtype != STQ_BF16))
+        return STQ_ERR_INVALID_ARG;
+    if (!(d == 16 || d == 32 || d == 64 || d == 128)) return STQ_ERR_UNSUPPORTED;
+    if (B == 0 || T == 0) return STQ_OK;
+    if (!states || !slots || !q || !k || !v || !alpha || !o) return STQ_ERR_INVALID_ARG;
+    if (!decay_aligned(states) || !decay_aligned(q) || !decay_aligned(k) || !decay_aligned(v) || !decay_aligned(o) ||
+        (reinterpret_cast<uintptr_t>(alpha) % 4) || (reinterpret_cast<uintptr_t>(slots) % 4))
+        return STQ_ERR_INVALID_ARG;
+    if (B > 2147483647 / H) return STQ_ERR_UNSUPPORTED;
+    *work = true;
+    return STQ_OK;
+}
+
+stq::DecayParams decay_params(int32_t B, int32_t H, int32_t T, float *states, int32_t state_slots,
+                              const int32_t *slots, const void *q, const void *k, const void *v, const float *alpha,
+                              const int32_t *lens, float *o, int32_t *dev_status)
+{
+    stq::DecayParams p{};
+    p.B = B;
+    p.H = H;
+    p.T = T;
+    p.states = states;
+    p.state_slots = state_slots;
+    p.slots = slots;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.alpha = alpha;
+    p.lens = lens;
+    p.o = o;
+    p.status = dev_status;
+    return p;
+}
+
+}  // namespace
+
+extern "C" stq_status stq_decay_step(int32_t B, int32_t H, int32_t d, int32_t in_dtype, float *states,
+                                     int32_t state_slots, const int32_t *slots, const void *q, const void *k,
+                                     const void *v, const float *alpha, float *o, int32_t *dev_status, void *stream)
+{
+    bool work;
+    const stq_status st = check_decay(B, H, 1, d, in_dtype, states, state_slots, slots, q, k, v, alpha, o, &work);
+    if (st != STQ_OK || !work) return st;
+    const stq::DecayParams p =
+        decay_params(B, H, 1, states, state_slots, slots, q, k, v, alpha, nullptr, o, dev_status);
+    const int bf = in_dtype == STQ_BF16;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    switch (d) {
+        case 16: e = stq::step<16>(p, bf, s); break;
+        case 32: e = stq::step<32>(p, bf, s); break;
+        case 64: e = stq::step<64>(p, bf, s); break;
+        default: e = stq::step<128>(p, bf, s); break;
+    }
+    return e == cudaSuccess ? STQ_OK : STQ_ERR_CUDA;
+}
+
+extern "C" size_t stq_decay_prefill_workspace_bytes(int32_t B, int32_t H, int32_t T, int32_t d, int32_t in_dtype)
+{
+    (void)B, (void)H, (void)T, (void)d, (void)in_dtype;
+    return 0;
+}
+
+extern "C" stq_status stq_decay_prefill(int32_t B, int32_t H, int32_t T, int32_t d, int32_t in_dtype, float *states,
+                                        int32_t state_slots, const int32_t *slots, const void *q, const void *k,
+                                        const void *v, const float *alpha, const int32_t *lens, float *o,
+                                        void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream)
+{
+    bool work;
+    const stq_status st = check_decay(B, H, T, d, in_dtype, states, state_slots, slots, q, k, v, alpha, o, &work);
+    if (st != STQ_OK || !work) return st;
+    if (reinterpret_cast<uintptr_t>(lens) % 4) return STQ_ERR_INVALID_ARG;
+    (void)workspace, (void)workspace_bytes;
+    const stq::DecayParams p =
+        decay_params(B, H, T, states, state_slots, slots, q, k, v, alpha, lens, o, dev_status);
+    return stq::launch_decay_serial(p, d, in_dtype == STQ_BF16, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? STQ_OK
+               : STQ_ERR_CUDA;
+}

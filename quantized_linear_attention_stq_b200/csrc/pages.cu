@@ -1,0 +1,244 @@
+// pages.cu -- the paged key-value cache's bookkeeping on the GPU (contract in include/stq.h): pages
+// for the new tokens of a batch (stq_page_plan) and the write of their keys and values
+// (stq_page_write).
+//
+// Plan. With page size ps, request b holds P(len_b) pages, P(n) = ceil(n / ps), and asks for
+// P(len_b + new_b) - P(len_b) more. Two prefix sums over the requests, of new tokens and of asked
+// pages, give every request its place in the slot map and in the free list, so the result does not
+// depend on the order in which threads run. One CTA walks the requests 1024 at a time: the call's
+// cost is launch and memory latency, not bytes.
+//
+// Write. A row of a token's keys (all heads) is contiguous on the way in; each head's part goes to
+// its own page rows. 16-byte copies, four in flight per thread; bound by HBM.
+#include "../../include/stq.h"
+#include "stq_internal.cuh"
+
+namespace stq {
+namespace {
+
+constexpr int NTP = 1024;
+
+struct PlanParams {
+    int32_t *table;
+    const int32_t *lens, *fresh, *free_pages, *free_head;
+    int32_t *slot_map, *starts, *lens_out, *head_out, *status;
+    int32_t B, W, page, F, N;
+    int fill;  // 1: this launch also writes the slot map's entries behind each request's first
+};
+
+// Inclusive prefix sums of a pair of 64-bit counts over the CTA; *total gets the CTA's sums.
+__device__ __forceinline__ longlong2 scan_pair(longlong2 x, longlong2 *warp_sums, longlong2 *total)
+{
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long a = __shfl_up_sync(0xffffffffu, x.x, d), b = __shfl_up_sync(0xffffffffu, x.y, d);
+        if (lane >= d) {
+            x.x += a;
+            x.y += b;
+        }
+    }
+    if (lane == 31) warp_sums[w] = x;
+    __syncthreads();
+    if (w == 0) {
+        longlong2 y = warp_sums[lane];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long a = __shfl_up_sync(0xffffffffu, y.x, d), b = __shfl_up_sync(0xffffffffu, y.y, d);
+            if (lane >= d) {
+                y.x += a;
+                y.y += b;
+            }
+        }
+        warp_sums[lane] = y;
+    }
+    __syncthreads();
+    if (w > 0) {
+        x.x += warp_sums[w - 1].x;
+        x.y += warp_sums[w - 1].y;
+    }
+    *total = warp_sums[31];
+    __syncthreads();
+    return x;
+}
+
+// Slot of the token at position pos of a request, from its table row; -1 (and the bounds flag) where
+// the row names no page whose slots are int32.
+__device__ __forceinline__ int slot_at(const int32_t *row, int pos, int page, int32_t *status)
+{
+    const int p = pos / page;
+    const long long slot = (long long)row[p] * page + (pos - p * page);
+    if (row[p] >= 0 && slot <= 0x7fffffffLL) return (int)slot;
+    flag(status, kFlagBounds);
+    return -1;
+}
+
+__global__ void __launch_bounds__(NTP) page_plan_kernel(const PlanParams p)
+{
+    __shared__ longlong2 warp_sums[32];
+    __shared__ int first[NTP + 1];  // slot-map index of each request's first token, in this block of requests
+    __shared__ int held[NTP];       // its length before, or -1: it gets no slots
+    __shared__ int most;            // pages taken by the requests served so far
+    const int tid = threadIdx.x;
+    const int head = *p.free_head;
+    const bool bad_head = head < 0 || head > p.F;
+    const long long avail = bad_head ? 0 : p.F - head;
+    long long tok0 = 0, page0 = 0;
+    if (tid == 0) {
+        most = 0;
+        if (bad_head) flag(p.status, kFlagBounds);
+    }
+    for (int b0 = 0; b0 < p.B; b0 += NTP) {
+        const int b = b0 + tid;
+        int len = 0, add = 0, now = 0, need = 0;
+        bool ok = false;
+        if (b < p.B) {
+            len = p.lens[b];
+            add = p.fresh[b];
+            ok = len >= 0 && add >= 0 && (long long)len + add <= (long long)p.W * p.page;
+            if (!ok) add = add < 0 ? 0 : add;
+            if (ok) {
+                now = (int)(((long long)len + p.page - 1) / p.page);
+                need = (int)(((long long)len + add + p.page - 1) / p.page) - now;
+            }
+        }
+        longlong2 total;
+        const longlong2 upto = scan_pair(make_longlong2(add, need), warp_sums, &total);
+        const long long tok = tok0 + upto.x - add, pg = page0 + upto.y - need;
+        if (b < p.B) {
+            // its pages are on the list, and its tokens in the slot map
+            const bool fits = ok && (need == 0 || pg + need <= avail) && tok + add <= p.N;
+            if (!fits) flag(p.status, kFlagBounds);
+            p.starts[b] = (int)(tok < p.N ? tok : p.N);
+            p.lens_out[b] = fits ? len + add : len;
+            int32_t *row = p.table + (size_t)b * p.W;
+            if (fits) {
+                if (need > 0) {
+                    atomicMax(&most, (int)(pg + need));
+                    for (int i = 0; i < need; ++i) row[now + i] = p.free_pages[head + pg + i];
+                }
+            }
+            held[tid] = fits ? len : -1;
+            first[tid] = (int)(tok < p.N ? tok : p.N);
+            // the entry that a later launch reads whether the request was served from
+            if (!p.fill && add > 0 && tok < p.N) p.slot_map[tok] = fits ? slot_at(row, len, p.page, p.status) : -1;
+        }
+        const long long end = tok0 + total.x < p.N ? tok0 + total.x : p.N;
+        if (p.fill) {
+            __syncthreads();
+            const int nb = p.B - b0 < NTP ? p.B - b0 : NTP;
+            for (long long i = tok0 + tid; i < end; i += NTP) {
+                int lo = 0, hi = nb;  // the last request of the block that starts at or before i
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (first[mid] <= i) lo = mid; else hi = mid;
+                }
+                const int32_t *row = p.table + (size_t)(b0 + lo) * p.W;
+                p.slot_map[i] = held[lo] < 0 ? -1 : slot_at(row, held[lo] + (int)(i - first[lo]), p.page, p.status);
+            }
+        }
+        __syncthreads();
+        tok0 = end;
+        page0 += total.y;
+    }
+    if (p.fill)
+        for (long long i = tok0 + tid; i < p.N; i += NTP) p.slot_map[i] = -1;
+    if (tid == 0) {
+        p.starts[p.B] = (int)tok0;
+        *p.head_out = bad_head ? head : head + most;
+    }
+}
+
+struct WriteParams {
+    uint8_t *k_pages, *v_pages;
+    const int32_t *slot_map;
+    const uint8_t *k, *v;
+    int64_t k_stride, v_stride;  // bytes between tokens
+    int32_t *status;
+    int64_t pieces;              // 16-byte pieces of one of k, v
+    int32_t heads, page, row_pieces, head_pieces;
+    int64_t slots;               // pages * page
+};
+
+__global__ void __launch_bounds__(256) page_write_kernel(const WriteParams p)
+{
+    const int64_t step = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < p.pieces; i += step) {
+        const int64_t t = i / p.row_pieces;
+        const int c = (int)(i - t * p.row_pieces), h = c / p.head_pieces, x = c - h * p.head_pieces;
+        const int slot = p.slot_map[t];
+        if (slot < 0 || slot >= p.slots) {
+            if (slot != -1) flag(p.status, kFlagBounds);
+            continue;
+        }
+        const int pg = slot / p.page, off = slot - pg * p.page;
+        const size_t dst = ((((size_t)pg * p.heads + h) * p.page + off) * p.head_pieces + x) * 16;
+        const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p.k + t * p.k_stride + c * 16));
+        const uint4 b = __ldcs(reinterpret_cast<const uint4 *>(p.v + t * p.v_stride + c * 16));
+        *reinterpret_cast<uint4 *>(p.k_pages + dst) = a;
+        *reinterpret_cast<uint4 *>(p.v_pages + dst) = b;
+    }
+}
+
+}  // namespace
+}  // namespace stq
+
+namespace {
+bool page_aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+}  // namespace
+
+extern "C" stq_status stq_page_plan(int32_t B, int32_t table_width, int32_t page_size, int32_t *table,
+                                    const int32_t *lens, const int32_t *fresh, const int32_t *free_pages,
+                                    int32_t num_free, const int32_t *free_head, int32_t *slot_map,
+                                    int32_t slot_map_size, int32_t *starts, int32_t *lens_out, int32_t *head_out,
+                                    int32_t *dev_status, void *stream)
+{
+    if (B < 0 || table_width < 0 || page_size < 1 || num_free < 0 || slot_map_size < 0) return STQ_ERR_INVALID_ARG;
+    if (!free_head || !head_out || !starts) return STQ_ERR_INVALID_ARG;
+    if ((slot_map_size > 0 && !slot_map) || (num_free > 0 && !free_pages)) return STQ_ERR_INVALID_ARG;
+    if (B > 0 && (!lens || !fresh || !lens_out || (table_width > 0 && !table))) return STQ_ERR_INVALID_ARG;
+    for (const void *ptr : {(const void *)table, (const void *)lens, (const void *)fresh, (const void *)free_pages,
+                            (const void *)free_head, (const void *)slot_map, (const void *)starts,
+                            (const void *)lens_out, (const void *)head_out})
+        if (!page_aligned(ptr, 4)) return STQ_ERR_INVALID_ARG;
+    stq::PlanParams p{table,  lens,     fresh,    free_pages, free_head,   slot_map,  starts, lens_out,
+                      head_out, dev_status, B, table_width, page_size, num_free, slot_map_size, 1};
+    stq::page_plan_kernel<<<1, stq::NTP, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    return cudaGetLastError() == cudaSuccess ? STQ_OK : STQ_ERR_CUDA;
+}
+
+extern "C" stq_status stq_page_write(int32_t N, int32_t kv_heads, int32_t d, int32_t dtype, int32_t page_size,
+                                     int32_t num_pages, void *k_pages, void *v_pages, const int32_t *slot_map,
+                                     const void *k, const void *v, int64_t k_stride, int64_t v_stride,
+                                     int32_t *dev_status, void *stream)
+{
+    if (N < 0 || kv_heads < 1 || page_size < 1 || num_pages < 0 || (dtype != STQ_F32 && dtype != STQ_BF16))
+        return STQ_ERR_INVALID_ARG;
+    if (!(d == 16 || d == 32 || d == 64 || d == 128)) return STQ_ERR_UNSUPPORTED;
+    if (N == 0) return STQ_OK;
+    if (!k_pages || !v_pages || !slot_map || !k || !v) return STQ_ERR_INVALID_ARG;
+    const int64_t size = dtype == STQ_BF16 ? 2 : 4, row = (int64_t)kv_heads * d;
+    if (!page_aligned(k_pages, 16) || !page_aligned(v_pages, 16) || !page_aligned(k, 16) || !page_aligned(v, 16) ||
+        !page_aligned(slot_map, 4) || k_stride < row || v_stride < row || k_stride * size % 16 != 0 ||
+        v_stride * size % 16 != 0)
+        return STQ_ERR_INVALID_ARG;
+    if (row * size / 16 > 0x7fffffff || (int64_t)num_pages * page_size > 0x7fffffff) return STQ_ERR_UNSUPPORTED;
+    stq::WriteParams p{};
+    p.k_pages = static_cast<uint8_t *>(k_pages);
+    p.v_pages = static_cast<uint8_t *>(v_pages);
+    p.slot_map = slot_map;
+    p.k = static_cast<const uint8_t *>(k);
+    p.v = static_cast<const uint8_t *>(v);
+    p.k_stride = k_stride * size;
+    p.v_stride = v_stride * size;
+    p.status = dev_status;
+    p.heads = kv_heads;
+    p.page = page_size;
+    p.head_pieces = (int)(d * size / 16);
+    p.row_pieces = kv_heads * p.head_pieces;
+    p.pieces = (int64_t)N * p.row_pieces;
+    p.slots = (int64_t)num_pages * page_size;
+    const int64_t want = (p.pieces + 255) / 256;
+    stq::page_write_kernel<<<(unsigned)(want < 65536 ? want : 65536), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    return cudaGetLastError() == cudaSuccess ? STQ_OK : STQ_ERR_CUDA;
+}

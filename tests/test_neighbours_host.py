@@ -1,0 +1,148 @@
+"""Host-side checks (no GPU) of the calls for the layers next to the quantized ones: decayed linear
+attention, page plans, cache writes and paged attention. Bad arguments are refused before anything is
+enqueued, so the pointers here are never dereferenced."""
+import ctypes
+
+import pytest
+import torch
+
+P = ctypes.c_void_p
+FAKE, ODD4, ODD2 = P(0x10000), P(0x10004), P(0x10002)
+OK, INVALID, UNSUPPORTED = 0, 1, 2
+
+
+@pytest.fixture(scope="module")
+def stq():
+    from quantized_linear_attention_stq_b200 import build
+
+    build.build()
+    import quantized_linear_attention_stq_b200 as m
+
+    return m
+
+
+def step(L, B=2, H=3, d=64, dt=1, states=FAKE, n=4, slots=FAKE, q=FAKE, k=FAKE, v=FAKE, alpha=FAKE, o=FAKE):
+    return L.stq_decay_step(B, H, d, dt, states, n, slots, q, k, v, alpha, o, None, None)
+
+
+def prefill(L, B=2, H=3, T=5, d=64, dt=1, states=FAKE, n=4, slots=FAKE, q=FAKE, k=FAKE, v=FAKE, alpha=FAKE, lens=None,
+            o=FAKE, ws=None, wsn=0):
+    return L.stq_decay_prefill(B, H, T, d, dt, states, n, slots, q, k, v, alpha, lens, o, ws, wsn, None, None)
+
+
+@pytest.mark.parametrize("call", [step, prefill])
+def test_decay_refusals(stq, call):
+    L = stq.lib()
+    for bad in (dict(B=-1), dict(H=0), dict(dt=2), dict(n=-1), dict(states=None), dict(slots=None), dict(q=None),
+                dict(k=None), dict(v=None), dict(alpha=None), dict(o=None), dict(states=ODD4), dict(q=ODD4),
+                dict(k=ODD4), dict(v=ODD4), dict(o=ODD4), dict(alpha=ODD2), dict(slots=ODD2)):
+        assert call(L, **bad) == INVALID, bad
+    for d in (0, 8, 96, 256):
+        assert call(L, d=d) == UNSUPPORTED
+    assert call(L, B=1 << 20, H=1 << 12) == UNSUPPORTED  # more (request, head) pairs than int32 counts
+    # no work: nothing is looked at
+    assert call(L, B=0, states=None, slots=None, q=None, k=None, v=None, alpha=None, o=None) == OK
+
+
+def test_decay_prefill_refusals(stq):
+    L = stq.lib()
+    assert prefill(L, T=-1) == INVALID
+    assert prefill(L, lens=ODD2) == INVALID
+    assert prefill(L, T=0, states=None, q=None, o=None) == OK
+    need = stq.decay_prefill_workspace_bytes(1, 2, 100000, 128, torch.bfloat16)
+    if need:
+        assert prefill(L, B=1, H=2, T=100000, d=128, ws=FAKE, wsn=need - 1) == INVALID
+        assert prefill(L, B=1, H=2, T=100000, d=128, ws=P(0x10010), wsn=need) == INVALID
+    for B, H, T, d in ((0, 2, 5, 64), (2, 0, 5, 64), (2, 2, 0, 64), (2, 2, 5, 63), (-1, -1, -1, -1)):
+        assert stq.decay_prefill_workspace_bytes(B, H, T, d, torch.bfloat16) == 0
+    with pytest.raises(TypeError):
+        stq.decay_prefill_workspace_bytes(1, 1, 1, 64, torch.float16)
+
+
+def plan(L, B=2, W=3, page=16, table=FAKE, lens=FAKE, fresh=FAKE, free=FAKE, F=9, head=FAKE, smap=FAKE, N=8,
+         starts=FAKE, lens_out=FAKE, head_out=FAKE):
+    return L.stq_page_plan(B, W, page, table, lens, fresh, free, F, head, smap, N, starts, lens_out, head_out, None, None)
+
+
+def test_plan_refusals(stq):
+    L = stq.lib()
+    for bad in (dict(B=-1), dict(W=-1), dict(page=0), dict(F=-1), dict(N=-1), dict(table=None), dict(lens=None),
+                dict(fresh=None), dict(free=None), dict(head=None), dict(smap=None), dict(starts=None),
+                dict(lens_out=None), dict(head_out=None), dict(table=ODD2), dict(lens=ODD2), dict(fresh=ODD2),
+                dict(free=ODD2), dict(head=ODD2), dict(smap=ODD2), dict(starts=ODD2), dict(lens_out=ODD2),
+                dict(head_out=ODD2)):
+        assert plan(L, **bad) == INVALID, bad
+
+
+def write(L, N=3, H=2, d=64, dt=1, page=16, n=5, kp=FAKE, vp=FAKE, smap=FAKE, k=FAKE, v=FAKE, ks=128, vs=128):
+    return L.stq_page_write(N, H, d, dt, page, n, kp, vp, smap, k, v, ks, vs, None, None)
+
+
+def test_write_refusals(stq):
+    L = stq.lib()
+    for bad in (dict(N=-1), dict(H=0), dict(dt=2), dict(page=0), dict(n=-1), dict(kp=None), dict(vp=None),
+                dict(smap=None), dict(k=None), dict(v=None), dict(kp=ODD4), dict(vp=ODD4), dict(k=ODD4), dict(v=ODD4),
+                dict(smap=ODD2), dict(ks=127), dict(vs=64), dict(ks=132), dict(vs=129)):
+        assert write(L, **bad) == INVALID, bad
+    assert write(L, d=48) == UNSUPPORTED
+    assert write(L, page=1 << 20, n=1 << 12) == UNSUPPORTED  # slots past int32
+    assert write(L, N=0, kp=None, vp=None, smap=None, k=None, v=None) == OK
+
+
+def attend(L, B=2, Hq=4, Hkv=2, d=64, dt=1, page=16, n=5, W=3, q=FAKE, kp=FAKE, vp=FAKE, table=FAKE, lens=FAKE,
+           scale=1.0, o=FAKE, ws=None, wsn=0):
+    return L.stq_paged_attention(B, Hq, Hkv, d, dt, page, n, W, q, kp, vp, table, lens, scale, o, ws, wsn, None, None)
+
+
+def test_attention_refusals(stq):
+    L = stq.lib()
+    for bad in (dict(B=-1), dict(Hq=0), dict(Hkv=0), dict(Hq=3), dict(dt=2), dict(page=0), dict(n=-1), dict(W=-1),
+                dict(q=None), dict(kp=None), dict(vp=None), dict(table=None), dict(lens=None), dict(o=None),
+                dict(q=ODD4), dict(kp=ODD4), dict(vp=ODD4), dict(o=ODD4), dict(table=ODD2), dict(lens=ODD2),
+                dict(scale=float("inf")), dict(scale=float("nan"))):
+        assert attend(L, **bad) == INVALID, bad
+    need = stq.paged_attention_workspace_bytes(2, 4, 64, 2)
+    assert need > 0 and need % 4 == 0
+    assert attend(L, ws=FAKE, wsn=need - 1) == INVALID
+    assert attend(L, ws=P(0x10010), wsn=need) == INVALID
+    assert attend(L, d=256) == UNSUPPORTED
+    assert attend(L, page=1 << 16, W=1 << 16) == UNSUPPORTED  # positions past int32
+    assert attend(L, B=0, q=None, kp=None, vp=None, table=None, lens=None, o=None) == OK
+    for args in ((0, 4, 64, 2), (2, 3, 64, 2), (2, 4, 64, 0), (2, 1, 64, 2)):
+        assert stq.paged_attention_workspace_bytes(*args) == 0
+
+
+def test_binding_checks(stq):
+    """Types, shapes, contiguity and device are checked before the library is called."""
+    f, i = torch.float32, torch.int32
+    z = lambda *s, t=f: torch.zeros(*s, dtype=t)  # noqa: E731
+    good = dict(states=z(3, 2, 16, 16), slots=z(1, t=i), q=z(1, 2, 16), k=z(1, 2, 16), v=z(1, 2, 16), alpha=z(1, 2),
+                o=z(1, 2, 16))
+    for name, t, err in (("q", z(2, 16), ValueError), ("k", z(1, 2, 32), ValueError), ("v", z(1, 2, 16, t=torch.bfloat16), TypeError),
+                         ("q", z(1, 2, 16, t=torch.float16), TypeError), ("states", z(2, 16, 16), ValueError),
+                         ("states", z(3, 1, 16, 16), ValueError), ("slots", z(2, t=i), ValueError),
+                         ("slots", z(1, t=torch.int64), TypeError), ("alpha", z(1, 1), ValueError),
+                         ("o", z(1, 2, 16, t=torch.bfloat16), TypeError), ("q", None, TypeError)):
+        with pytest.raises(err):
+            stq.decay_step(**{**good, name: t})
+    with pytest.raises(ValueError):  # everything in order, but not on a CUDA device
+        stq.decay_step(**good)
+    with pytest.raises(ValueError):
+        stq.decay_prefill(**good)
+    k = z(4, 2, 16)
+    pages = z(3, 2, 8, 16)
+    for bad in (dict(k=z(4, 2, 32)[..., ::2]), dict(v=z(4, 1, 16)), dict(k_pages=z(3, 1, 8, 16)),
+                dict(v_pages=z(3, 2, 8, 32)), dict(slot_map=z(3, t=i)), dict(k=z(1, 2, 16).expand(4, 2, 16))):
+        with pytest.raises(ValueError):
+            stq.page_write(**{**dict(k_pages=pages, v_pages=pages, slot_map=z(4, t=i), k=k, v=k), **bad})
+    att = dict(q=z(2, 4, 16), k_pages=pages, v_pages=pages, table=z(2, 5, t=i), lens=z(2, t=i), o=z(2, 4, 16), scale=1.0)
+    for bad in (dict(q=z(8, 16)), dict(table=z(3, 5, t=i)), dict(lens=z(3, t=i)), dict(o=z(2, 4, 8)),
+                dict(v_pages=z(2, 2, 8, 16)), dict(workspace=z(1)), dict(q=z(2, 16, 4).transpose(1, 2))):
+        with pytest.raises(ValueError):
+            stq.paged_attention(**{**att, **bad})
+    pl = dict(table=z(2, 5, t=i), lens=z(2, t=i), fresh=z(2, t=i), free_pages=z(9, t=i), free_head=z(1, t=i),
+              slot_map=z(8, t=i), starts=z(3, t=i), lens_out=z(2, t=i), head_out=z(1, t=i), page_size=4)
+    for bad in (dict(table=z(10, t=i)), dict(lens=z(3, t=i)), dict(starts=z(2, t=i)), dict(free_pages=z(3, 3, t=i)),
+                dict(head_out=z(2, t=i))):
+        with pytest.raises(ValueError):
+            stq.page_plan(**{**pl, **bad})
