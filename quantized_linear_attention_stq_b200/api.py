@@ -54,6 +54,8 @@ _lib_handle = None
 def lib() -> ctypes.CDLL:
     """Load libstq.so (raises if it has not been built)."""
     global _lib_handle
+    if _lib_handle is not None:
+        return _lib_handle
     with _lock:
         if _lib_handle is None:
             if not os.path.exists(LIB_PATH):
@@ -127,6 +129,9 @@ def _stream(stream) -> ctypes.c_void_p:
 
 
 def _need(t: torch.Tensor, name: str, dtype, shape, device=None):
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and (device is None or t.device == device) and t.is_contiguous()):
+        return  # the usual case in one test: the calls' host time is what small steps wait for
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -340,12 +345,12 @@ def _call(fn, what: str, dev: torch.device, status, stream, *args):
         raise ValueError(f"{what}: tensors are on {dev}, expected a CUDA device")
     if status is not None:
         _need(status, "status", torch.int32, (1,), dev)
-    here = torch.cuda.current_device()
-    if dev.index is None or dev.index == here:
-        st = fn(*args, None if status is None else status.data_ptr(), _stream(stream))
+        status = status.data_ptr()
+    if dev.index == torch._C._cuda_getDevice():
+        st = fn(*args, status, torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, None if status is None else status.data_ptr(), _stream(stream))
+            st = fn(*args, status, _stream(stream))
     if st != STQ_OK:
         raise StqError(st, what)
 

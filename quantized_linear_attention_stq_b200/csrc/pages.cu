@@ -5,8 +5,11 @@
 // Plan. With page size ps, request b holds P(len_b) pages, P(n) = ceil(n / ps), and asks for
 // P(len_b + new_b) - P(len_b) more. Two prefix sums over the requests, of new tokens and of asked
 // pages, give every request its place in the slot map and in the free list, so the result does not
-// depend on the order in which threads run. One CTA walks the requests 1024 at a time: the call's
-// cost is launch and memory latency, not bytes.
+// depend on the order in which threads run. Bound by launch and memory latency, not by bytes. A small
+// plan is one block's, in one launch. A large one takes two: many blocks, each of which makes the
+// sums for itself and writes its part of the table and of the slot map, then one block that writes
+// the lengths, the starts and the list's head, which the first launch still reads when they are
+// updated in place.
 //
 // Write. A row of a token's keys (all heads) is contiguous on the way in; each head's part goes to
 // its own page rows. 16-byte copies, four in flight per thread; bound by HBM.
@@ -17,13 +20,15 @@ namespace stq {
 namespace {
 
 constexpr int NTP = 1024;
+constexpr int kPlanOneBlock = 4096;
 
 struct PlanParams {
     int32_t *table;
     const int32_t *lens, *fresh, *free_pages, *free_head;
     int32_t *slot_map, *starts, *lens_out, *head_out, *status;
     int32_t B, W, page, F, N;
-    int fill;  // 1: this launch also writes the slot map's entries behind each request's first
+    int fill;    // this launch writes the table and the slot map
+    int commit;  // this launch (of one block) writes the lengths, the starts and the list's head
 };
 
 // Inclusive prefix sums of a pair of 64-bit counts over the CTA; *total gets the CTA's sums.
@@ -62,90 +67,108 @@ __device__ __forceinline__ longlong2 scan_pair(longlong2 x, longlong2 *warp_sums
     return x;
 }
 
-// Slot of the token at position pos of a request, from its table row; -1 (and the bounds flag) where
-// the row names no page whose slots are int32.
-__device__ __forceinline__ int slot_at(const int32_t *row, int pos, int page, int32_t *status)
+// Slot of row `row` of page pg; -1 (and the bounds flag) for a page whose slots are not int32.
+__device__ __forceinline__ int slot_of(int pg, int row, int page, int32_t *status)
 {
-    const int p = pos / page;
-    const long long slot = (long long)row[p] * page + (pos - p * page);
-    if (row[p] >= 0 && slot <= 0x7fffffffLL) return (int)slot;
+    const long long slot = (long long)pg * page + row;
+    if (pg >= 0 && slot <= 0x7fffffffLL) return (int)slot;
     flag(status, kFlagBounds);
     return -1;
+}
+
+// The last of n ascending starts that is at or before i.
+__device__ __forceinline__ int find_start(const int *start, int n, long long i)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= i) lo = mid; else hi = mid;
+    }
+    return lo;
 }
 
 __global__ void __launch_bounds__(NTP) page_plan_kernel(const PlanParams p)
 {
     __shared__ longlong2 warp_sums[32];
-    __shared__ int first[NTP + 1];  // slot-map index of each request's first token, in this block of requests
-    __shared__ int held[NTP];       // its length before, or -1: it gets no slots
-    __shared__ int most;            // pages taken by the requests served so far
+    // of the requests of one round, NTP at a time:
+    __shared__ int token0[NTP];  // slot-map index of the first new token
+    __shared__ int held[NTP];    // tokens before, or -1: it gets no slots
+    __shared__ int page0[NTP];   // pages asked for by the round's requests before it
+    __shared__ int taken;        // pages taken by the requests served so far
     const int tid = threadIdx.x;
     const int head = *p.free_head;
     const bool bad_head = head < 0 || head > p.F;
     const long long avail = bad_head ? 0 : p.F - head;
-    long long tok0 = 0, page0 = 0;
+    const bool speaks = p.commit != 0;  // one launch of a call reports what it finds
+    long long tok_base = 0, page_base = 0;
     if (tid == 0) {
-        most = 0;
-        if (bad_head) flag(p.status, kFlagBounds);
+        taken = 0;
+        if (bad_head && speaks) flag(p.status, kFlagBounds);
     }
+    const int step = (int)gridDim.x * NTP, at = (int)blockIdx.x * NTP + tid;
     for (int b0 = 0; b0 < p.B; b0 += NTP) {
-        const int b = b0 + tid;
-        int len = 0, add = 0, now = 0, need = 0;
+        const int b = b0 + tid, nb = min(NTP, p.B - b0);
+        int len = 0, add = 0, need = 0;
         bool ok = false;
         if (b < p.B) {
             len = p.lens[b];
             add = p.fresh[b];
             ok = len >= 0 && add >= 0 && (long long)len + add <= (long long)p.W * p.page;
-            if (!ok) add = add < 0 ? 0 : add;
-            if (ok) {
-                now = (int)(((long long)len + p.page - 1) / p.page);
-                need = (int)(((long long)len + add + p.page - 1) / p.page) - now;
-            }
+            add = max(add, 0);
+            if (ok)
+                need = (int)(((long long)len + add + p.page - 1) / p.page - ((long long)len + p.page - 1) / p.page);
         }
         longlong2 total;
         const longlong2 upto = scan_pair(make_longlong2(add, need), warp_sums, &total);
-        const long long tok = tok0 + upto.x - add, pg = page0 + upto.y - need;
+        const long long tok = tok_base + upto.x - add, pg = page_base + upto.y - need;
         if (b < p.B) {
             // its pages are on the list, and its tokens in the slot map
             const bool fits = ok && (need == 0 || pg + need <= avail) && tok + add <= p.N;
-            if (!fits) flag(p.status, kFlagBounds);
-            p.starts[b] = (int)(tok < p.N ? tok : p.N);
-            p.lens_out[b] = fits ? len + add : len;
-            int32_t *row = p.table + (size_t)b * p.W;
-            if (fits) {
-                if (need > 0) {
-                    atomicMax(&most, (int)(pg + need));
-                    for (int i = 0; i < need; ++i) row[now + i] = p.free_pages[head + pg + i];
+            token0[tid] = (int)min(tok, (long long)p.N);
+            held[tid] = fits ? len : -1;
+            page0[tid] = (int)min(upto.y - need, 0x7fffffffLL);
+            if (fits && need > 0) atomicMax(&taken, (int)(pg + need));
+            if (!fits && speaks) flag(p.status, kFlagBounds);
+            if (p.commit) {
+                p.starts[b] = token0[tid];
+                p.lens_out[b] = fits ? len + add : len;
+            }
+        }
+        const long long end = min(tok_base + total.x, (long long)p.N);
+        __syncthreads();
+        if (p.fill) {
+            // the list's pages of this round: those of one request go to its row, in order
+            const long long pages = min(total.y, avail - page_base);
+            for (long long i = at; i < pages; i += step) {
+                const int r = find_start(page0, nb, i);
+                if (held[r] >= 0) {
+                    const int now = (int)(((long long)held[r] + p.page - 1) / p.page);
+                    p.table[(size_t)(b0 + r) * p.W + now + (int)(i - page0[r])] = p.free_pages[head + page_base + i];
                 }
             }
-            held[tid] = fits ? len : -1;
-            first[tid] = (int)(tok < p.N ? tok : p.N);
-            // the entry that a later launch reads whether the request was served from
-            if (!p.fill && add > 0 && tok < p.N) p.slot_map[tok] = fits ? slot_at(row, len, p.page, p.status) : -1;
-        }
-        const long long end = tok0 + total.x < p.N ? tok0 + total.x : p.N;
-        if (p.fill) {
-            __syncthreads();
-            const int nb = p.B - b0 < NTP ? p.B - b0 : NTP;
-            for (long long i = tok0 + tid; i < end; i += NTP) {
-                int lo = 0, hi = nb;  // the last request of the block that starts at or before i
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (first[mid] <= i) lo = mid; else hi = mid;
+            for (long long i = tok_base + at; i < end; i += step) {
+                const int r = find_start(token0, nb, i);
+                int slot = -1;
+                if (held[r] >= 0) {
+                    const int pos = held[r] + (int)(i - token0[r]), k = pos / p.page;
+                    const int now = (int)(((long long)held[r] + p.page - 1) / p.page);
+                    // a page it held before, or one just taken (its entry may not be written yet)
+                    const int pgid = k < now ? p.table[(size_t)(b0 + r) * p.W + k]
+                                             : p.free_pages[head + page_base + page0[r] + (k - now)];
+                    slot = slot_of(pgid, pos - k * p.page, p.page, p.status);
                 }
-                const int32_t *row = p.table + (size_t)(b0 + lo) * p.W;
-                p.slot_map[i] = held[lo] < 0 ? -1 : slot_at(row, held[lo] + (int)(i - first[lo]), p.page, p.status);
+                p.slot_map[i] = slot;
             }
         }
         __syncthreads();
-        tok0 = end;
-        page0 += total.y;
+        tok_base = end;
+        page_base += total.y;
     }
     if (p.fill)
-        for (long long i = tok0 + tid; i < p.N; i += NTP) p.slot_map[i] = -1;
-    if (tid == 0) {
-        p.starts[p.B] = (int)tok0;
-        *p.head_out = bad_head ? head : head + most;
+        for (long long i = tok_base + at; i < p.N; i += step) p.slot_map[i] = -1;
+    if (p.commit && tid == 0) {
+        p.starts[p.B] = (int)tok_base;
+        *p.head_out = bad_head ? head : head + taken;
     }
 }
 
@@ -201,9 +224,21 @@ extern "C" stq_status stq_page_plan(int32_t B, int32_t table_width, int32_t page
                             (const void *)free_head, (const void *)slot_map, (const void *)starts,
                             (const void *)lens_out, (const void *)head_out})
         if (!page_aligned(ptr, 4)) return STQ_ERR_INVALID_ARG;
-    stq::PlanParams p{table,  lens,     fresh,    free_pages, free_head,   slot_map,  starts, lens_out,
-                      head_out, dev_status, B, table_width, page_size, num_free, slot_map_size, 1};
-    stq::page_plan_kernel<<<1, stq::NTP, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    stq::PlanParams p{table,    lens,       fresh, free_pages,  free_head, slot_map, starts,        lens_out,
+                      head_out, dev_status, B,     table_width, page_size, num_free, slot_map_size, 1,  1};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // the slot map's size bounds the work: one block up to kPlanOneBlock entries
+    if (slot_map_size <= stq::kPlanOneBlock) {
+        stq::page_plan_kernel<<<1, stq::NTP, 0, s>>>(p);
+        return cudaGetLastError() == cudaSuccess ? STQ_OK : STQ_ERR_CUDA;
+    }
+    const int blocks = (slot_map_size + stq::NTP - 1) / stq::NTP;
+    p.commit = 0;
+    stq::page_plan_kernel<<<blocks < 296 ? blocks : 296, stq::NTP, 0, s>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return STQ_ERR_CUDA;
+    p.fill = 0;
+    p.commit = 1;
+    stq::page_plan_kernel<<<1, stq::NTP, 0, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? STQ_OK : STQ_ERR_CUDA;
 }
 
