@@ -7,6 +7,11 @@
 // the maximum from m to m', what was summed so far is scaled by exp(m - m'). Exponentials are taken
 // in base 2, with scale * log2(e) multiplied into the scores. Bound by HBM: every cached key and
 // value is read once for all the query heads that share it.
+//
+// bf16 caches go through the warp-level matrix instructions (16 query rows x 16 keys): with one new
+// token a unit has 16 rows at most, an eighth of what a tcgen05 tile is tall, and the products are
+// a small part of the time that the bytes take. Weights enter the second product as bf16 terms
+// whose sum is the fp32 weight, so that o keeps fp32's accuracy. fp32 caches go through fp32 FMAs.
 #include "../../include/stq.h"
 #include "stq_paged.cuh"
 
@@ -108,7 +113,7 @@ struct SimtSmem {
 // One unit's tiles [t0, t1): scores by quarters of d (a lane per key, a warp per quarter), softmax
 // by rows, products by (columns, key class). Leaves the sums in acc, joined over the key classes, in
 // shared memory (sums[GT][D]), and m, l.
-template <int D, int GT, int IN_BF16>
+template <int D, int GT>
 __device__ __forceinline__ void simt_unit(const Params &p, SimtSmem<D, GT> &sm, int b, int hk, int rt, int len,
                                           int t0, int t1, float *sums)
 {
@@ -118,7 +123,7 @@ __device__ __forceinline__ void simt_unit(const Params &p, SimtSmem<D, GT> &sm, 
     const int rows = min(GT, p.group - rt * ROWS);
     const size_t q0 = ((size_t)b * p.Hq + (size_t)hk * p.group + rt * ROWS) * D;
     __syncthreads();  // the unit before has been read out
-    for (int i = tid; i < GT * D; i += NTA) (&sm.q[0][0])[i] = i < rows * D ? load_in<IN_BF16>(p.q, q0 + i) : 0.f;
+    for (int i = tid; i < GT * D; i += NTA) (&sm.q[0][0])[i] = i < rows * D ? ((const float *)p.q)[q0 + i] : 0.f;
     if (tid < GT) {
         sm.m[tid] = -INFINITY;
         sm.l[tid] = 0.f;
@@ -140,17 +145,8 @@ __device__ __forceinline__ void simt_unit(const Params &p, SimtSmem<D, GT> &sm, 
                 const int pg = row[t / p.page];
                 if (pg >= 0 && pg < p.num_pages) {
                     const size_t at = (((size_t)pg * p.Hkv + hk) * p.page + t % p.page) * D + 4 * c;
-                    if constexpr (IN_BF16) {
-                        const uint2 a = *reinterpret_cast<const uint2 *>((const __nv_bfloat16 *)p.k_pages + at);
-                        const uint2 e = *reinterpret_cast<const uint2 *>((const __nv_bfloat16 *)p.v_pages + at);
-                        kk = make_float4(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xFFFF0000u),
-                                         __uint_as_float(a.y << 16), __uint_as_float(a.y & 0xFFFF0000u));
-                        vv = make_float4(__uint_as_float(e.x << 16), __uint_as_float(e.x & 0xFFFF0000u),
-                                         __uint_as_float(e.y << 16), __uint_as_float(e.y & 0xFFFF0000u));
-                    } else {
-                        kk = *reinterpret_cast<const float4 *>((const float *)p.k_pages + at);
-                        vv = *reinterpret_cast<const float4 *>((const float *)p.v_pages + at);
-                    }
+                    kk = *reinterpret_cast<const float4 *>((const float *)p.k_pages + at);
+                    vv = *reinterpret_cast<const float4 *>((const float *)p.v_pages + at);
                     live = 1.f;
                 } else {
                     flag(p.status, kFlagBounds);
@@ -233,10 +229,316 @@ __device__ __forceinline__ void simt_unit(const Params &p, SimtSmem<D, GT> &sm, 
     __syncthreads();
 }
 
+// ---------------------------------------------------------------------------------------------
+// bf16 caches
+// ---------------------------------------------------------------------------------------------
+constexpr int SUB = 16;  // keys of a warp's step; the block's four warps take a tile's four quarters
+static_assert(TK == SUB * (NTA / 32), "a tile is one step of every warp");
+
+// How the three bf16 terms of the weights (h + m + l, 24 significand bits) are laid on the 16 rows:
+// rows of the query tile that a group leaves free take further terms of the same rows, whose
+// scores are computed alongside.
+//   group <= 4: rows 0..3 h, 4..7 m, 8..11 l   one product
+//   group <= 8: rows 0..7 h, 8..15 m; then l   two products
+//   else:       three products
+template <int GROUP>
+struct Terms {
+    static constexpr int PERIOD = GROUP;  // row % PERIOD is the query head
+    static constexpr int PRODUCTS = GROUP == 4 ? 1 : GROUP == 8 ? 2 : 3;
+};
+
+template <int D>
+struct MmaCfg {
+    static constexpr int CH = D / 8;                   // 16-byte chunks of a row
+    static constexpr int HALF = SUB * D * 2;           // bytes of a step's keys (or values)
+    static constexpr int STAGES = D == 128 ? 3 : 4;
+    static constexpr int WARP_BYTES = STAGES * 2 * HALF;
+    static constexpr int RING = (NTA / 32) * WARP_BYTES;
+    static constexpr int SUMS = (NTA / 32) * ROWS * (D + 4) * 4;  // the warps' sums, where the ring was
+    static constexpr int MAIN = RING > SUMS ? RING : SUMS;
+    static constexpr int OUT = ROWS * D * 4;
+    static constexpr int SMEM = MAIN + OUT + (NTA / 32 + 1) * ROWS * 2 * 4 + (NTA / 32) * STAGES * 4;
+};
+
+// Byte offset of chunk c of row r: rows of 128 bytes or more are swizzled by r % 8, shorter ones by
+// their 128-byte line, so that 8 rows' same chunk falls on 8 different 16-byte banks.
+template <int D>
+__device__ __forceinline__ uint32_t row_chunk(int r, int c)
+{
+    constexpr int CH = MmaCfg<D>::CH, PER = CH >= 8 ? 1 : 8 / CH, MASK = (CH >= 8 ? 8 : CH) - 1;
+    return (uint32_t)(r * CH + (c ^ ((r / PER) & MASK))) * 16u;
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t bf2(float x, float y)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+// What rounding (x, y) to the packed bf16 pair v leaves over.
+__device__ __forceinline__ void rest2(uint32_t v, float &x, float &y)
+{
+    x -= __uint_as_float(v << 16);
+    y -= __uint_as_float(v & 0xFFFF0000u);
+}
+
+// One unit's tiles [t0, t1): every warp takes its 16 keys of each tile through its own ring of
+// asynchronous copies and keeps its own maximum, sum and products; joined at the end into
+// sums[ROWS][D], m, l (shared memory).
+template <int D, int GROUP>
+__device__ __forceinline__ void mma_unit(const Params &p, uint8_t *smem, int b, int hk, int rt, int len, int t0, int t1,
+                                         float *sums, float *m_out, float *l_out)
+{
+    using M = MmaCfg<D>;
+    using T = Terms<GROUP>;
+    constexpr int KS = D / 16, NT = D / 8, PC = SUB * M::CH / 32;  // k steps, column tiles, copies of a lane
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, r = lane >> 2, qd = lane & 3;
+    const int rows = min(ROWS, p.group - rt * ROWS);
+    const uint32_t ring = smem_u32(smem) + (uint32_t)w * M::WARP_BYTES;
+    float *wm = l_out + ROWS, *wl = wm + (NTA / 32) * ROWS;  // the warps' maxima and sums
+    volatile uint32_t *masks = reinterpret_cast<uint32_t *>(wl + (NTA / 32) * ROWS) + w * M::STAGES;
+    __syncthreads();  // the unit before has been read out
+
+    uint32_t qa[KS][4];
+    {
+        const __nv_bfloat16 *q = (const __nv_bfloat16 *)p.q + ((size_t)b * p.Hq + (size_t)hk * p.group + rt * ROWS) * D;
+        const int g0 = r % T::PERIOD, g1 = (r + 8) % T::PERIOD;
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int col = 16 * k + 8 * h + 2 * qd;
+                qa[k][2 * h] = g0 < rows ? *reinterpret_cast<const uint32_t *>(q + g0 * D + col) : 0u;
+                qa[k][2 * h + 1] = g1 < rows ? *reinterpret_cast<const uint32_t *>(q + g1 * D + col) : 0u;
+            }
+    }
+    float acc[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // of rows r and r + 8; sums per lane
+
+    const int32_t *row = p.table + (size_t)b * p.W;
+    const int steps = t1 - t0;
+    const size_t head = (size_t)hk * p.page;
+    // the page of this lane's key (lanes 16.. repeat 0..) at a step; -1 behind the end
+    auto page_at = [&](int j) {
+        const int t = (t0 + j) * TK + w * SUB + (lane & 15);
+        return j < steps && t < len ? row[t / p.page] : -1;
+    };
+    // copy a step's keys and values into ring slot `slot`
+    auto fetch = [&](int j, int slot, int pg) {
+        const int t = (t0 + j) * TK + w * SUB + (lane & 15);
+        const bool in = j < steps && t < len, live = in && pg >= 0 && pg < p.num_pages;
+        if (in && !live) flag(p.status, kFlagBounds);
+        const uint32_t mask = __ballot_sync(0xffffffffu, live);
+        const size_t at = live ? ((size_t)pg * p.Hkv * p.page + head + t % p.page) * D : 0;
+        if (lane == 0) masks[slot] = mask & 0xffffu;
+        const uint32_t dst = ring + (uint32_t)slot * (2 * M::HALF);
+#pragma unroll
+        for (int i = 0; i < PC; ++i) {
+            const int c = i * 32 + lane, kr = c / M::CH, ch = c % M::CH;
+            const size_t src = __shfl_sync(0xffffffffu, (unsigned long long)at, kr) + ch * 8;
+            const bool ok = (mask >> kr) & 1u;
+            cp16(dst + row_chunk<D>(kr, ch), (const __nv_bfloat16 *)p.k_pages + src, ok);
+            cp16(dst + M::HALF + row_chunk<D>(kr, ch), (const __nv_bfloat16 *)p.v_pages + src, ok);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    int pg = page_at(0);
+#pragma unroll
+    for (int j = 0; j < M::STAGES - 1; ++j) {
+        const int next = page_at(j + 1);
+        fetch(j, j, pg);
+        pg = next;
+    }
+    int slot = 0;
+    for (int j = 0; j < steps; ++j) {
+        const int next = page_at(j + M::STAGES);
+        asm volatile("cp.async.wait_group %0;" ::"n"(M::STAGES - 2) : "memory");
+        __syncwarp();
+        const uint32_t mask = masks[slot];
+        const uint32_t kb = ring + (uint32_t)slot * (2 * M::HALF), vb = kb + M::HALF;
+        // scores of 16 keys: two column tiles of 8, even and odd k steps in chains of their own
+        float s[2][2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[h][n][e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            uint32_t f[4];  // keys 0..7 (chunks 2k, 2k + 1), keys 8..15
+            ldsm4(f, kb + row_chunk<D>((lane & 7) + (lane >> 4) * 8, 2 * k + ((lane >> 3) & 1)));
+            mma16816(s[k & 1][0], qa[k], f[0], f[1]);
+            mma16816(s[k & 1][1], qa[k], f[2], f[3]);
+        }
+        float x[2][4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool live = (mask >> (8 * n + 2 * qd + (e & 1))) & 1u;
+                x[n][e] = live ? (s[0][n][e] + s[1][n][e]) * p.scale2 : -INFINITY;
+            }
+        float u0 = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
+        float u1 = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+            u0 = fmaxf(u0, __shfl_xor_sync(0xffffffffu, u0, d));
+            u1 = fmaxf(u1, __shfl_xor_sync(0xffffffffu, u1, d));
+        }
+        const float n0 = fmaxf(m0, u0), n1 = fmaxf(m1, u1);
+        const float c0 = n0 == -INFINITY ? 1.f : exp2f(m0 - n0), c1 = n1 == -INFINITY ? 1.f : exp2f(m1 - n1);
+        m0 = n0;
+        m1 = n1;
+        l0 *= c0;
+        l1 *= c1;
+        const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            x[n][0] = exp2f(x[n][0] - b0);
+            x[n][1] = exp2f(x[n][1] - b0);
+            x[n][2] = exp2f(x[n][2] - b1);
+            x[n][3] = exp2f(x[n][3] - b1);
+            l0 += x[n][0] + x[n][1];
+            l1 += x[n][2] + x[n][3];
+        }
+        // the weights' terms as rows of the first operand: keys 0..7 in a[0], a[1], keys 8..15 in a[2], a[3]
+        uint32_t ta[3][4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float &y0 = x[n][2 * h], &y1 = x[n][2 * h + 1];
+                const uint32_t t0b = bf2(y0, y1);
+                rest2(t0b, y0, y1);
+                const uint32_t t1b = bf2(y0, y1);
+                rest2(t1b, y0, y1);
+                const uint32_t t2b = bf2(y0, y1);
+                const int at = 2 * n + h;
+                if constexpr (GROUP == 4) {
+                    ta[0][at] = h == 0 ? (r < 4 ? t0b : t1b) : (r < 4 ? t2b : 0u);
+                } else if constexpr (GROUP == 8) {
+                    ta[0][at] = h == 0 ? t0b : t1b;
+                    ta[1][at] = h == 0 ? t2b : 0u;
+                } else {
+                    ta[0][at] = t0b;
+                    ta[1][at] = t1b;
+                    ta[2][at] = t2b;
+                }
+            }
+        // Products of one step go to sums of their own, which are added to the running ones by fp32
+        // FMAs with the rescaling: the matrix instruction truncates the sum it is given, and over a
+        // long cache that bias adds up (500,001 keys: 4.3e-6 of the result, against 6e-7 this way).
+        constexpr int NB = NT < 4 ? NT : 4;  // column tiles at a time, so that the terms' chains overlap
+#pragma unroll
+        for (int n = 0; n < NT; n += NB) {
+            float y[NB][4];
+            uint32_t f[NB / 2][4];  // columns 8n.. : keys 0..7, 8..15; columns 8n + 8.. : the same
+#pragma unroll
+            for (int i = 0; i < NB / 2; ++i) ldsm4t(f[i], vb + row_chunk<D>(lane & 15, n + 2 * i + (lane >> 4)));
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[i][e] = 0.f;
+#pragma unroll
+            for (int t = T::PRODUCTS - 1; t >= 0; --t)
+#pragma unroll
+                for (int i = 0; i < NB; ++i) mma16816(y[i], ta[t], f[i / 2][2 * (i & 1)], f[i / 2][2 * (i & 1) + 1]);
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                acc[n + i][0] = fmaf(acc[n + i][0], c0, y[i][0]);
+                acc[n + i][1] = fmaf(acc[n + i][1], c0, y[i][1]);
+                acc[n + i][2] = fmaf(acc[n + i][2], c1, y[i][2]);
+                acc[n + i][3] = fmaf(acc[n + i][3], c1, y[i][3]);
+            }
+        }
+        __syncwarp();  // every lane has read the slot that is filled next
+        const int fill = slot == 0 ? M::STAGES - 1 : slot - 1;
+        fetch(j + M::STAGES - 1, fill, pg);
+        pg = next;
+        slot = slot + 1 == M::STAGES ? 0 : slot + 1;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+    }
+    __syncthreads();  // the rings are done with
+    float *ws = reinterpret_cast<float *>(smem) + w * (ROWS * (D + 4));
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        *reinterpret_cast<float2 *>(ws + r * (D + 4) + 8 * n + 2 * qd) = make_float2(acc[n][0], acc[n][1]);
+        *reinterpret_cast<float2 *>(ws + (r + 8) * (D + 4) + 8 * n + 2 * qd) = make_float2(acc[n][2], acc[n][3]);
+    }
+    if (qd == 0) {
+        wm[w * ROWS + r] = m0;
+        wm[w * ROWS + r + 8] = m1;
+        wl[w * ROWS + r] = l0;
+        wl[w * ROWS + r + 8] = l1;
+    }
+    __syncthreads();
+    // join the four warps, and the terms that lie on rows of their own
+    const float *all = reinterpret_cast<const float *>(smem);
+    constexpr int TERM_ROWS = GROUP == 4 ? 3 : GROUP == 8 ? 2 : 1;
+    for (int i = tid; i < rows * D; i += NTA) {
+        const int g = i / D, c = i % D;
+        float m = wm[g];
+#pragma unroll
+        for (int v = 1; v < NTA / 32; ++v) m = fmaxf(m, wm[v * ROWS + g]);
+        const float base = m == -INFINITY ? 0.f : m;
+        float sum = 0.f, l = 0.f;
+#pragma unroll
+        for (int v = 0; v < NTA / 32; ++v) {
+            const float e = exp2f(wm[v * ROWS + g] - base);
+            float part = 0.f;
+#pragma unroll
+            for (int t = TERM_ROWS - 1; t >= 0; --t) part += all[(v * ROWS + g + t * GROUP) * (D + 4) + c];
+            sum = fmaf(e, part, sum);
+            l = fmaf(e, wl[v * ROWS + g], l);
+        }
+        sums[i] = sum;
+        if (c == 0) {
+            m_out[g] = m;
+            l_out[g] = l;
+        }
+    }
+    __syncthreads();
+}
+
 // Writes a finished unit's output, or a piece of it for the join.
 template <int D>
-__device__ __forceinline__ void finish(const Params &p, int b, int hk, int rt, int len, const float *sums,
-                                       const float *m, const float *l, int piece)
+__device__ __forceinline__ void finish(const Params &p, int b, int hk, int rt, const float *sums, const float *m,
+                                       const float *l, int piece)
 {
     const int rows = min(ROWS, p.group - rt * ROWS);
     if (piece >= 0) {
@@ -259,20 +561,17 @@ __device__ __forceinline__ void finish(const Params &p, int b, int hk, int rt, i
     if (bad) flag(p.status, kFlagNonfinite);
 }
 
-template <int D, int GT, int IN_BF16>
-__global__ void __launch_bounds__(NTA) paged_simt_kernel(const Params p)
+// Calls unit(b, hk, rt, len, first tile, end tile, piece) for the block's work.
+template <class Unit>
+__device__ __forceinline__ void walk(const Params &p, Unit unit)
 {
-    extern __shared__ __align__(16) uint8_t raw[];
-    SimtSmem<D, GT> &sm = *reinterpret_cast<SimtSmem<D, GT> *>(raw);
-    float *sums = &sm.k[0][0];  // a unit's sums are joined where its keys were
     const int units = p.Hkv * p.row_tiles;
     if (!p.split) {
         const int u = blockIdx.x % units, b = blockIdx.x / units;
         bool bad;
         const int len = cached_length(p, b, &bad);
         if (bad && threadIdx.x == 0) flag(p.status, kFlagBounds);
-        simt_unit<D, GT, IN_BF16>(p, sm, b, u / p.row_tiles, u % p.row_tiles, len, 0, tiles_of(len), sums);
-        finish<D>(p, b, u / p.row_tiles, u % p.row_tiles, len, sums, sm.m, sm.l, -1);
+        unit(b, u / p.row_tiles, u % p.row_tiles, len, 0, tiles_of(len), -1);
         return;
     }
     const Cursor cur = find_share(p, units);
@@ -284,14 +583,35 @@ __global__ void __launch_bounds__(NTA) paged_simt_kernel(const Params p)
         while (at < cur.end && at < r0 + (long long)nt * units) {
             const int u = (int)((at - r0) / nt);
             const long long s = r0 + (long long)u * nt, e = s + nt, stop = e < cur.end ? e : cur.end;
-            simt_unit<D, GT, IN_BF16>(p, sm, b, u / p.row_tiles, u % p.row_tiles, len, (int)(at - s), (int)(stop - s),
-                                      sums);
-            const bool whole = at == s && stop == e;
-            finish<D>(p, b, u / p.row_tiles, u % p.row_tiles, len, sums, sm.m, sm.l, whole ? -1 : s < cur.begin ? 0 : 1);
+            unit(b, u / p.row_tiles, u % p.row_tiles, len, (int)(at - s), (int)(stop - s),
+                 at == s && stop == e ? -1 : s < cur.begin ? 0 : 1);
             at = stop;
         }
         before += nt;
     }
+}
+
+template <int D, int GT>
+__global__ void __launch_bounds__(NTA) paged_simt_kernel(const Params p)
+{
+    extern __shared__ __align__(16) uint8_t raw[];
+    SimtSmem<D, GT> &sm = *reinterpret_cast<SimtSmem<D, GT> *>(raw);
+    float *sums = &sm.k[0][0];  // a unit's sums are joined where its keys were
+    walk(p, [&](int b, int hk, int rt, int len, int t0, int t1, int piece) {
+        simt_unit<D, GT>(p, sm, b, hk, rt, len, t0, t1, sums);
+        finish<D>(p, b, hk, rt, sums, sm.m, sm.l, piece);
+    });
+}
+
+template <int D, int GROUP>
+__global__ void __launch_bounds__(NTA, 2) paged_mma_kernel(const Params p)
+{
+    extern __shared__ __align__(128) uint8_t raw[];
+    float *sums = reinterpret_cast<float *>(raw + MmaCfg<D>::MAIN), *m = sums + ROWS * D, *l = m + ROWS;
+    walk(p, [&](int b, int hk, int rt, int len, int t0, int t1, int piece) {
+        mma_unit<D, GROUP>(p, raw, b, hk, rt, len, t0, t1, sums, m, l);
+        finish<D>(p, b, hk, rt, sums, m, l, piece);
+    });
 }
 
 // Joins the pieces of the units that were cut, and zeroes the rows of requests without tokens.
@@ -334,11 +654,9 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const Params p, int d, 
     o[c] = out;
 }
 
-template <int D, int GT>
-cudaError_t launch_simt(const Params &p, int in_bf16, unsigned grid, cudaStream_t s)
+template <class Kernel>
+cudaError_t launch_one(Kernel kernel, const Params &p, unsigned grid, int bytes, cudaStream_t s)
 {
-    const auto kernel = in_bf16 ? paged_simt_kernel<D, GT, 1> : paged_simt_kernel<D, GT, 0>;
-    constexpr int bytes = (int)sizeof(SimtSmem<D, GT>);
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     kernel<<<grid, NTA, bytes, s>>>(p);
@@ -346,21 +664,27 @@ cudaError_t launch_simt(const Params &p, int in_bf16, unsigned grid, cudaStream_
 }
 
 template <int D>
-cudaError_t launch_group(const Params &p, int in_bf16, unsigned grid, cudaStream_t s)
+cudaError_t launch_d(const Params &p, int in_bf16, unsigned grid, cudaStream_t s)
 {
     const int g = p.group;
-    return g <= 1 ? launch_simt<D, 1>(p, in_bf16, grid, s)
-         : g <= 4 ? launch_simt<D, 4>(p, in_bf16, grid, s)
-                  : launch_simt<D, 16>(p, in_bf16, grid, s);
+    if (in_bf16) {
+        constexpr int bytes = MmaCfg<D>::SMEM;
+        return g <= 4   ? launch_one(paged_mma_kernel<D, 4>, p, grid, bytes, s)
+               : g <= 8 ? launch_one(paged_mma_kernel<D, 8>, p, grid, bytes, s)
+                        : launch_one(paged_mma_kernel<D, 16>, p, grid, bytes, s);
+    }
+    return g <= 1   ? launch_one(paged_simt_kernel<D, 1>, p, grid, (int)sizeof(SimtSmem<D, 1>), s)
+           : g <= 4 ? launch_one(paged_simt_kernel<D, 4>, p, grid, (int)sizeof(SimtSmem<D, 4>), s)
+                    : launch_one(paged_simt_kernel<D, 16>, p, grid, (int)sizeof(SimtSmem<D, 16>), s);
 }
 
 cudaError_t launch_attention(const Params &p, int d, int in_bf16, unsigned grid, cudaStream_t s)
 {
     switch (d) {
-        case 16: return launch_group<16>(p, in_bf16, grid, s);
-        case 32: return launch_group<32>(p, in_bf16, grid, s);
-        case 64: return launch_group<64>(p, in_bf16, grid, s);
-        default: return launch_group<128>(p, in_bf16, grid, s);
+        case 16: return launch_d<16>(p, in_bf16, grid, s);
+        case 32: return launch_d<32>(p, in_bf16, grid, s);
+        case 64: return launch_d<64>(p, in_bf16, grid, s);
+        default: return launch_d<128>(p, in_bf16, grid, s);
     }
 }
 
@@ -428,7 +752,7 @@ extern "C" stq_status stq_paged_attention(int32_t B, int32_t q_heads, int32_t kv
         p.first_tile = static_cast<long long *>(workspace);
         p.pieces = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + prefix_bytes(B));
         const int64_t most = units * ((span + stq::paged::TK - 1) / stq::paged::TK);
-        grid = 4 * (int64_t)sms;
+        grid = (dtype == STQ_BF16 ? 2 : 4) * (int64_t)sms;  // the blocks that fit at a time
         if (grid > stq::paged::kMaxBlocks) grid = stq::paged::kMaxBlocks;
         if (grid > most) grid = most > 0 ? most : 1;
     }
