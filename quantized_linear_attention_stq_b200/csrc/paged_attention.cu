@@ -56,8 +56,8 @@ __device__ __forceinline__ Cursor find_share(const Params &p, int units)
 #pragma unroll
     for (int i = 0; i < NTA / 32; ++i) total += red[i];
     total *= units;
-    const long long begin = share_begin(total, blockIdx.x, gridDim.x);
-    const long long end = share_begin(total, blockIdx.x + 1, gridDim.x);
+    const int C = busy_blocks(total, gridDim.x), c = min((int)blockIdx.x, C);
+    const long long begin = share_begin(total, c, C), end = share_begin(total, min(c + 1, C), C);
     __syncthreads();
     long long before = 0;
     if (tid == 0) {
@@ -574,6 +574,7 @@ __device__ __forceinline__ void walk(const Params &p, Unit unit)
         unit(b, u / p.row_tiles, u % p.row_tiles, len, 0, tiles_of(len), -1);
         return;
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up; it waits
     const Cursor cur = find_share(p, units);
     long long at = cur.begin, before = cur.before;
     for (int b = cur.b; at < cur.end; ++b) {
@@ -614,44 +615,69 @@ __global__ void __launch_bounds__(NTA, 2) paged_mma_kernel(const Params p)
     });
 }
 
-// Joins the pieces of the units that were cut, and zeroes the rows of requests without tokens.
-// One block per (request, query head), a thread per column.
-__global__ void __launch_bounds__(128) paged_join_kernel(const Params p, int d, int blocks)
+// Joins the pieces of the units that were cut, and zeroes the rows of requests without tokens. One
+// block per (request, query head): d columns x NTJ / d classes of pieces, joined in a fixed order.
+constexpr int NTJ = 256;
+__global__ void __launch_bounds__(NTJ) paged_join_kernel(const Params p, int d, int most_blocks)
 {
+    __shared__ float weight[kMaxBlocks], red[NTJ], lsum[NTJ];
+    // started while the attention kernel runs; every thread waits for its end, so that what follows
+    // on the stream follows both
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int units = p.Hkv * p.row_tiles;
-    const int row = blockIdx.x % p.Hq, b = blockIdx.x / p.Hq;
-    const int hk = row / p.group, g = row % p.group, rt = g / ROWS, r = g % ROWS, c = threadIdx.x;
+    const int row = blockIdx.x % p.Hq, b = blockIdx.x / p.Hq, tid = threadIdx.x;
+    const int hk = row / p.group, g = row % p.group, rt = g / ROWS, r = g % ROWS;
     const long long f0 = p.first_tile[b], nt = p.first_tile[b + 1] - f0, total = p.first_tile[p.B] * units;
     float *o = p.o + ((size_t)b * p.Hq + row) * d;
     if (nt == 0) {
-        if (c < d) o[c] = 0.f;
+        if (tid < d) o[tid] = 0.f;
         return;
     }
+    const int blocks = busy_blocks(total, most_blocks);
     const long long s = f0 * units + (hk * p.row_tiles + rt) * nt;
-    const int c0 = block_of(total, s, blocks), c1 = block_of(total, s + nt - 1, blocks);
-    if (c0 == c1 || c >= d) return;
+    const int c0 = block_of(total, s, blocks), n = block_of(total, s + nt - 1, blocks) - c0 + 1;
+    if (n == 1) return;  // finished by that block
+    // the unit goes on behind the first block's share, and began before the others'
     const size_t stride = (size_t)ROWS * (d + 2);
-    // the first block's piece goes on behind its share unless the unit began before it
-    auto piece = [&](int blk) {
-        const int which = s < share_begin(total, blk, blocks) ? 0 : 1;
-        return p.pieces + ((size_t)blk * 2 + which) * stride;
-    };
+    const float *first = p.pieces + (size_t)c0 * 2 * stride;
+    auto piece = [&](int i) { return first + (i == 0 ? stride : 2 * stride * i); };
     float m = -INFINITY;
-    for (int blk = c0; blk <= c1; ++blk)
-        if (share_begin(total, blk, blocks) < share_begin(total, blk + 1, blocks))
-            m = fmaxf(m, piece(blk)[ROWS * d + r]);
-    const float base = m == -INFINITY ? 0.f : m;
-    float sum = 0.f, l = 0.f;
-    for (int blk = c0; blk <= c1; ++blk)
-        if (share_begin(total, blk, blocks) < share_begin(total, blk + 1, blocks)) {
-            const float *x = piece(blk);
-            const float e = exp2f(x[ROWS * d + r] - base);
-            sum = fmaf(e, x[r * d + c], sum);
-            l = fmaf(e, x[ROWS * d + ROWS + r], l);
+    for (int i = tid; i < n; i += NTJ) m = fmaxf(m, weight[i] = piece(i)[ROWS * d + r]);
+    red[tid] = m;
+    __syncthreads();
+#pragma unroll
+    for (int h = NTJ / 2; h > 0; h >>= 1) {
+        if (tid < h) red[tid] = fmaxf(red[tid], red[tid + h]);
+        __syncthreads();
+    }
+    const float base = red[0] == -INFINITY ? 0.f : red[0];
+    __syncthreads();
+    float l = 0.f;
+    for (int i = tid; i < n; i += NTJ) {
+        weight[i] = exp2f(weight[i] - base);
+        l = fmaf(weight[i], piece(i)[ROWS * d + ROWS + r], l);
+    }
+    lsum[tid] = l;
+    __syncthreads();
+    const int c = tid % d, cls = tid / d, classes = NTJ / d;
+    float sum = 0.f;
+#pragma unroll 8
+    for (int i = cls; i < n; i += classes) sum = fmaf(weight[i], piece(i)[r * d + c], sum);
+    red[tid] = sum;
+    __syncthreads();
+#pragma unroll
+    for (int h = NTJ / 2; h > 0; h >>= 1) {
+        if (tid < h) {
+            lsum[tid] += lsum[tid + h];
+            if (h >= d) red[tid] += red[tid + h];
         }
-    const float out = l == 0.f ? 0.f : sum / l;
-    if (!(fabsf(out) <= 3.402823466e38f)) flag(p.status, kFlagNonfinite);
-    o[c] = out;
+        __syncthreads();
+    }
+    if (tid < d) {
+        const float out = lsum[0] == 0.f ? 0.f : red[tid] / lsum[0];
+        if (!(fabsf(out) <= 3.402823466e38f)) flag(p.status, kFlagNonfinite);
+        o[tid] = out;
+    }
 }
 
 template <class Kernel>
@@ -758,6 +784,15 @@ extern "C" stq_status stq_paged_attention(int32_t B, int32_t q_heads, int32_t kv
     }
     if (stq::launch_attention(p, d, dtype == STQ_BF16, (unsigned)grid, s) != cudaSuccess) return STQ_ERR_CUDA;
     if (!p.split) return STQ_OK;
-    stq::paged_join_kernel<<<(unsigned)((int64_t)B * q_heads), 128, 0, s>>>(p, d, (int)grid);
-    return cudaGetLastError() == cudaSuccess ? STQ_OK : STQ_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)((int64_t)B * q_heads));
+    cfg.blockDim = dim3(stq::NTJ);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, stq::paged_join_kernel, p, d, (int)grid);
+    return e == cudaSuccess ? STQ_OK : STQ_ERR_CUDA;
 }

@@ -42,6 +42,8 @@ __device__ __forceinline__ int cached_length(const Params &p, int b, bool *bad)
 }
 __device__ __forceinline__ int tiles_of(int len) { return (int)(((long long)len + TK - 1) / TK); }
 
+// Blocks that get work: each a tile at least.
+__device__ __forceinline__ int busy_blocks(long long W, int most) { return W < most ? (W > 0 ? (int)W : 1) : most; }
 // First tile of block c's share of W tiles over C blocks, and the block that holds tile t.
 __device__ __forceinline__ long long share_begin(long long W, int c, int C) { return W * c / C; }
 __device__ __forceinline__ int block_of(long long W, long long t, int C) { return (int)(((t + 1) * C - 1) / W); }
