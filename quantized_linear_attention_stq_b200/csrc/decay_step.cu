@@ -8,9 +8,14 @@
 // its store, all loads of a thread in flight at once; a warp's lanes hold consecutive columns, so
 // rows move in whole 128-byte lines and the readout is a sum over the CTA's row groups.
 //
-// Token by token. The state of a block of columns stays in registers for the whole prompt (columns
+// Token by token (fp32 inputs, short prompts). The state of a block of columns stays in registers for the whole prompt (columns
 // of S are independent of each other); tokens are staged through shared memory 32 at a time. A
 // column's rows are spread over SL lanes, joined by shuffles per token.
+//
+// Segments. Where there are too few heads to fill the GPU, prompts are cut into segments: a first
+// pass over all but the last makes each segment's own sum (from an empty state) and the product of its
+// decays, a join turns these into the states before the segments, and the main pass then runs all
+// segments at once. The first pass costs a part of the main one, so a cut has to win more than that.
 #include "../../include/stq.h"
 #include "stq_decay.cuh"
 
@@ -109,14 +114,14 @@ struct SerialCfg {
     static constexpr int TB = 32;                       // tokens staged at a time
 };
 
-template <int D, int IN_BF16>
+template <int D, int IN_BF16, int SUMS>
 __global__ void __launch_bounds__(SerialCfg<D>::NT) decay_serial_kernel(const DecayParams p)
 {
     using S = SerialCfg<D>;
     __shared__ __align__(16) float qs[S::TB][D], ks[S::TB][D];
     __shared__ float vs[S::TB][S::CB], os[S::TB][S::CB], as[S::TB];
     const int tid = threadIdx.x, r = tid % S::SL, cl = tid / S::SL;
-    const int c0 = blockIdx.x * S::CB;
+    const int seg = blockIdx.x / (D / S::CB), c0 = blockIdx.x % (D / S::CB) * S::CB;
     const size_t tile = blockIdx.y + (size_t)blockIdx.z * gridDim.y;  // (request, head)
     if (tile >= (size_t)p.B * p.H) return;
     const int b = (int)(tile / (unsigned)p.H), h = (int)(tile - (size_t)b * p.H);
@@ -126,17 +131,23 @@ __global__ void __launch_bounds__(SerialCfg<D>::NT) decay_serial_kernel(const De
         if (tid == 0) flag(p.status, kFlagBounds);
         return;
     }
-    if (len == 0) return;
-    float *st = p.states + ((size_t)slot * p.H + h) * (D * D) + c0 + cl;
+    const int64_t from = (int64_t)seg * p.seg_tokens;
+    if (from >= len) return;
+    const int end = len - (int)from < p.seg_tokens ? len : (int)from + p.seg_tokens;
+    if (SUMS && end == len) return;  // the state behind the last segment is the main pass's
+    float *pool = p.states + ((size_t)slot * p.H + h) * (D * D) + c0 + cl;
+    float *record = p.records ? p.records + (tile * p.segments + seg) * (D * D) + c0 + cl : nullptr;
+    const float *before = p.segments > 1 ? record : pool;
     // rows of a lane: groups of 4, SL groups apart, so that the lanes' 16-byte reads of k and q are adjacent
     float s[S::RW];
 #pragma unroll
-    for (int i = 0; i < S::RW; ++i) s[i] = st[(size_t)((i / 4 * S::SL + r) * 4 + i % 4) * D];
+    for (int i = 0; i < S::RW; ++i) s[i] = SUMS ? 0.f : before[(size_t)((i / 4 * S::SL + r) * 4 + i % 4) * D];
     const size_t base = tile * (size_t)p.T;
-    for (int t0 = 0; t0 < len; t0 += S::TB) {
-        const int n = len - t0 < S::TB ? len - t0 : S::TB;
+    double upto = 1.0;
+    for (int t0 = (int)from; t0 < end; t0 += S::TB) {
+        const int n = end - t0 < S::TB ? end - t0 : S::TB;
         for (int i = tid; i < n * D; i += S::NT) {
-            (&qs[0][0])[i] = load_in<IN_BF16>(p.q, (base + t0) * D + i);
+            if (!SUMS) (&qs[0][0])[i] = load_in<IN_BF16>(p.q, (base + t0) * D + i);
             (&ks[0][0])[i] = load_in<IN_BF16>(p.k, (base + t0) * D + i);
         }
         for (int i = tid; i < n * S::CB; i += S::NT)
@@ -146,25 +157,31 @@ __global__ void __launch_bounds__(SerialCfg<D>::NT) decay_serial_kernel(const De
 #pragma unroll 4
         for (int t = 0; t < n; ++t) {
             const float a = as[t], v = vs[t][cl];
+            if (SUMS) upto *= a;
             float acc = 0.f;
 #pragma unroll
             for (int i = 0; i < S::RW; i += 4) {
                 const float4 k4 = *reinterpret_cast<const float4 *>(&ks[t][(i / 4 * S::SL + r) * 4]);
-                const float4 q4 = *reinterpret_cast<const float4 *>(&qs[t][(i / 4 * S::SL + r) * 4]);
                 s[i] = fmaf(a, s[i], k4.x * v);
                 s[i + 1] = fmaf(a, s[i + 1], k4.y * v);
                 s[i + 2] = fmaf(a, s[i + 2], k4.z * v);
                 s[i + 3] = fmaf(a, s[i + 3], k4.w * v);
-                acc = fmaf(q4.x, s[i], acc);
-                acc = fmaf(q4.y, s[i + 1], acc);
-                acc = fmaf(q4.z, s[i + 2], acc);
-                acc = fmaf(q4.w, s[i + 3], acc);
+                if constexpr (!SUMS) {
+                    const float4 q4 = *reinterpret_cast<const float4 *>(&qs[t][(i / 4 * S::SL + r) * 4]);
+                    acc = fmaf(q4.x, s[i], acc);
+                    acc = fmaf(q4.y, s[i + 1], acc);
+                    acc = fmaf(q4.z, s[i + 2], acc);
+                    acc = fmaf(q4.w, s[i + 3], acc);
+                }
             }
+            if constexpr (!SUMS) {
 #pragma unroll
-            for (int m = S::SL / 2; m > 0; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
-            if (r == 0) os[t][cl] = acc;
+                for (int m = S::SL / 2; m > 0; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
+                if (r == 0) os[t][cl] = acc;
+            }
         }
         __syncthreads();
+        if constexpr (SUMS) continue;
         float bad = 0.f;
         for (int i = tid; i < n * S::CB; i += S::NT) {
             const float x = os[i / S::CB][i % S::CB];
@@ -174,13 +191,50 @@ __global__ void __launch_bounds__(SerialCfg<D>::NT) decay_serial_kernel(const De
         if (bad != 0.f) flag(p.status, kFlagNonfinite);
         // os is next written behind the next block's staging barrier, so no third barrier is needed
     }
-    float bad = 0.f;
+    if (!SUMS && end != len) return;
+    float *to = SUMS ? record : pool, bad = 0.f;
 #pragma unroll
     for (int i = 0; i < S::RW; ++i) {
-        st[(size_t)((i / 4 * S::SL + r) * 4 + i % 4) * D] = s[i];
+        to[(size_t)((i / 4 * S::SL + r) * 4 + i % 4) * D] = s[i];
         bad += s[i] - s[i];
     }
     if (bad != 0.f) flag(p.status, kFlagNonfinite);
+    if (SUMS && tid == 0 && c0 == 0) p.products[tile * p.segments + seg] = (float)upto;
+}
+
+// records[j] <- the state before segment j, for the segments that the prompt has. A thread per four
+// entries goes along the segments; its loads of JOIN segments are in flight at once.
+constexpr int JOIN = 8;
+__global__ void __launch_bounds__(256) decay_join_kernel(const DecayParams p, const int d)
+{
+    const int n4 = d * d / 4, per = (n4 + 255) / 256;
+    const int64_t tile = blockIdx.x / per;
+    const int i = blockIdx.x % per * 256 + threadIdx.x;
+    const int b = (int)(tile / p.H), h = (int)(tile - (int64_t)b * p.H);
+    const int slot = p.slots[b], len = prompt_length(p, b);
+    if (i >= n4 || slot < 0 || slot >= p.state_slots || len <= 0) return;
+    const int n = (int)(((int64_t)len + p.seg_tokens - 1) / p.seg_tokens);
+    float4 S = reinterpret_cast<const float4 *>(p.states + ((size_t)slot * p.H + h) * d * d)[i];
+    float4 *rec = reinterpret_cast<float4 *>(p.records + (size_t)tile * p.segments * d * d) + i;
+    const float *prod = p.products + tile * p.segments;
+    for (int j0 = 0; j0 < n; j0 += JOIN) {
+        float4 x[JOIN];
+        float a[JOIN];
+#pragma unroll
+        for (int j = 0; j < JOIN; ++j)
+            if (j0 + j < n - 1) {  // the last segment has no sum of its own
+                x[j] = rec[(size_t)(j0 + j) * n4];
+                a[j] = prod[j0 + j];
+            }
+#pragma unroll
+        for (int j = 0; j < JOIN; ++j)
+            if (j0 + j < n) {
+                rec[(size_t)(j0 + j) * n4] = S;
+                if (j0 + j < n - 1)
+                    S = make_float4(fmaf(a[j], S.x, x[j].x), fmaf(a[j], S.y, x[j].y), fmaf(a[j], S.z, x[j].z),
+                                    fmaf(a[j], S.w, x[j].w));
+            }
+    }
 }
 
 template <int D>
@@ -194,28 +248,80 @@ cudaError_t step(const DecayParams &p, int in_bf16, cudaStream_t s)
     return cudaGetLastError();
 }
 
-template <int D>
-cudaError_t serial(const DecayParams &p, int in_bf16, cudaStream_t s)
+template <int D, int IN_BF16>
+cudaError_t serial(const DecayParams &p, bool sums, cudaStream_t s)
 {
     const size_t tiles = (size_t)p.B * p.H;
     const unsigned gy = (unsigned)(tiles < 32768 ? tiles : 32768);
-    const dim3 grid(D / SerialCfg<D>::CB, gy, (unsigned)((tiles + gy - 1) / gy));
-    if (in_bf16)
-        decay_serial_kernel<D, 1><<<grid, SerialCfg<D>::NT, 0, s>>>(p);
+    const dim3 grid((unsigned)p.segments * (D / SerialCfg<D>::CB), gy, (unsigned)((tiles + gy - 1) / gy));
+    if (sums)
+        decay_serial_kernel<D, IN_BF16, 1><<<grid, SerialCfg<D>::NT, 0, s>>>(p);
     else
-        decay_serial_kernel<D, 0><<<grid, SerialCfg<D>::NT, 0, s>>>(p);
+        decay_serial_kernel<D, IN_BF16, 0><<<grid, SerialCfg<D>::NT, 0, s>>>(p);
     return cudaGetLastError();
+}
+
+cudaError_t decay_join(const DecayParams &p, int d, cudaStream_t s)
+{
+    const int64_t grid = (int64_t)p.B * p.H * ((d * d / 4 + 255) / 256);
+    decay_join_kernel<<<(unsigned)grid, 256, 0, s>>>(p, d);
+    return cudaGetLastError();
+}
+
+// How a prompt is done: by chunks or token by token, in how many segments of how many tokens.
+struct Split {
+    bool chunk;
+    int segments, seg_tokens;
+};
+
+constexpr int kSMs = 148;            // the workspace's size must not depend on the device in use
+constexpr int kMostSegments = 1024;  // the join goes along them
+
+Split split(int B, int H, int T, int d, int in_bf16, bool cut)
+{
+    Split r{in_bf16 && T >= 64, 1, T};
+    const int64_t tiles = (int64_t)B * H;
+    if (r.chunk) {
+        // one CTA to an SM: rounds of CTAs times chunks of each, the first pass at 2/5 of the main
+        // one, the two launches more at three chunks
+        const int64_t chunks = ((int64_t)T + kDecayChunk - 1) / kDecayChunk, ctas = tiles * (d > 64 ? 2 : 1);
+        double best = 0.0;
+        int64_t per = chunks;
+        for (int64_t n = 1; n <= (cut ? 64 : 1) && n <= chunks; ++n) {
+            const int64_t c = (chunks + n - 1) / n;
+            if ((chunks + c - 1) / c != n) continue;  // fewer segments of this length do
+            const double t = (double)((ctas * n + kSMs - 1) / kSMs) * c * (n > 1 ? 1.4 : 1.0) + (n > 1 ? 3.0 : 0.0);
+            if (n == 1 || t < best) best = t, per = c;
+        }
+        r.segments = (int)((chunks + per - 1) / per);
+        r.seg_tokens = (int)(per * kDecayChunk < 0x7fffffff ? per * kDecayChunk : 0x7fffff80);
+        return r;
+    }
+    const int64_t ctas = tiles * (d > 32 ? d / 32 : 1);
+    if (!cut || T < 128 || ctas > 2 * kSMs) return r;
+    int64_t n = 6 * kSMs / ctas;
+    n = n < T / 64 ? n : T / 64;
+    n = n < kMostSegments ? n : kMostSegments;
+    const int64_t per = (((int64_t)T + n - 1) / n + 31) / 32 * 32;
+    r.segments = (int)((T + per - 1) / per);
+    r.seg_tokens = (int)per;
+    return r;
+}
+
+size_t split_bytes(const Split &r, int B, int H, int d)
+{
+    return r.segments > 1 ? (size_t)B * H * r.segments * ((size_t)d * d + 1) * sizeof(float) : 0;
 }
 
 }  // namespace
 
-cudaError_t launch_decay_serial(const DecayParams &p, int d, int in_bf16, cudaStream_t s)
+cudaError_t launch_decay_serial(const DecayParams &p, int d, int in_bf16, bool sums, cudaStream_t s)
 {
     switch (d) {
-        case 16: return serial<16>(p, in_bf16, s);
-        case 32: return serial<32>(p, in_bf16, s);
-        case 64: return serial<64>(p, in_bf16, s);
-        default: return serial<128>(p, in_bf16, s);
+        case 16: return in_bf16 ? serial<16, 1>(p, sums, s) : serial<16, 0>(p, sums, s);
+        case 32: return in_bf16 ? serial<32, 1>(p, sums, s) : serial<32, 0>(p, sums, s);
+        case 64: return in_bf16 ? serial<64, 1>(p, sums, s) : serial<64, 0>(p, sums, s);
+        default: return in_bf16 ? serial<128, 1>(p, sums, s) : serial<128, 0>(p, sums, s);
     }
 }
 
@@ -290,8 +396,9 @@ extern "C" stq_status stq_decay_step(int32_t B, int32_t H, int32_t d, int32_t in
 
 extern "C" size_t stq_decay_prefill_workspace_bytes(int32_t B, int32_t H, int32_t T, int32_t d, int32_t in_dtype)
 {
-    (void)B, (void)H, (void)T, (void)d, (void)in_dtype;
-    return 0;
+    if (B < 1 || H < 1 || T < 1 || B > 2147483647 / H || (in_dtype != STQ_F32 && in_dtype != STQ_BF16)) return 0;
+    if (!(d == 16 || d == 32 || d == 64 || d == 128)) return 0;
+    return stq::split_bytes(stq::split(B, H, T, d, in_dtype == STQ_BF16, true), B, H, d);
 }
 
 extern "C" stq_status stq_decay_prefill(int32_t B, int32_t H, int32_t T, int32_t d, int32_t in_dtype, float *states,
@@ -303,10 +410,29 @@ extern "C" stq_status stq_decay_prefill(int32_t B, int32_t H, int32_t T, int32_t
     const stq_status st = check_decay(B, H, T, d, in_dtype, states, state_slots, slots, q, k, v, alpha, o, &work);
     if (st != STQ_OK || !work) return st;
     if (reinterpret_cast<uintptr_t>(lens) % 4) return STQ_ERR_INVALID_ARG;
-    (void)workspace, (void)workspace_bytes;
-    const stq::DecayParams p =
-        decay_params(B, H, T, states, state_slots, slots, q, k, v, alpha, lens, o, dev_status);
-    return stq::launch_decay_serial(p, d, in_dtype == STQ_BF16, static_cast<cudaStream_t>(stream)) == cudaSuccess
-               ? STQ_OK
-               : STQ_ERR_CUDA;
+    const int bf = in_dtype == STQ_BF16;
+    const size_t need = stq_decay_prefill_workspace_bytes(B, H, T, d, in_dtype);
+    if (workspace && need && (workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 256))
+        return STQ_ERR_INVALID_ARG;
+    const stq::Split cut = stq::split(B, H, T, d, bf, workspace != nullptr);
+    stq::DecayParams p = decay_params(B, H, T, states, state_slots, slots, q, k, v, alpha, lens, o, dev_status);
+    p.segments = cut.segments;
+    p.seg_tokens = cut.seg_tokens;
+    if (cut.segments > 1) {
+        p.records = static_cast<float *>(workspace);
+        p.products = p.records + (size_t)B * H * cut.segments * d * d;
+    }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    auto pass = [&](bool sums) {
+        cudaError_t e = cut.chunk ? stq::launch_decay_chunk(p, d, sums, s) : cudaErrorNotSupported;
+        if (e == cudaErrorNotSupported) e = stq::launch_decay_serial(p, d, bf, sums, s);
+        return e;
+    };
+    cudaError_t e = cudaSuccess;
+    if (cut.segments > 1) {
+        e = pass(true);
+        if (e == cudaSuccess) e = stq::decay_join(p, d, s);
+    }
+    if (e == cudaSuccess) e = pass(false);
+    return e == cudaSuccess ? STQ_OK : STQ_ERR_CUDA;
 }

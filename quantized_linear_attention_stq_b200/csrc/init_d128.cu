@@ -16,9 +16,8 @@
 // element; only the order of the column-energy sums differs.
 #include <cstddef>
 
-#include <cuda.h>
-
 #include "stq_internal.cuh"
+#include "tensor_map.cuh"
 
 namespace stq {
 namespace {
@@ -391,25 +390,6 @@ __global__ void __launch_bounds__(NTI, 1)
         for (int s = 0; s < NSI; ++s)
             if (sm.last[s] >= 0) mbar_wait_bounded(smem_u32(&sm.bars[s]), (uint32_t)(sm.last[s] / NSI) & 1u);
     }
-}
-
-// cuTensorMapEncodeTiled from the driver, looked up once through the runtime.
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled()
-{
-    // a function-local static: initialised once, safely across host threads
-    static const EncodeTiled fn = []() -> EncodeTiled {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            return reinterpret_cast<EncodeTiled>(f);
-        return nullptr;
-    }();
-    return fn;
 }
 
 }  // namespace

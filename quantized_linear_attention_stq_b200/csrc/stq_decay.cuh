@@ -14,10 +14,20 @@ struct DecayParams {
     float *o;             // [B][H][T][d]
     int32_t *status;
     int32_t state_slots, B, H, T;
+    // a prompt cut into segments (one: the whole prompt, records and products are null)
+    float *records;   // [B][H][segments][d][d]: a segment's own sum, then the state before it
+    float *products;  // [B][H][segments]: the product of a segment's decays
+    int32_t segments, seg_tokens;
 };
 
 // Token by token, any d and input type.
-cudaError_t launch_decay_serial(const DecayParams &p, int d, int in_bf16, cudaStream_t s);
+cudaError_t launch_decay_serial(const DecayParams &p, int d, int in_bf16, bool sums, cudaStream_t s);
+// Chunks of kDecayChunk tokens on the tensor cores, bf16 inputs, any d; cudaErrorNotSupported where no
+// tensor map can be made. seg_tokens is a multiple of kDecayChunk.
+// Both: with `sums`, the segments' own sums and products go to records and products, and nothing else
+// is written; without, the outputs and final states are, from the states before the segments.
+constexpr int kDecayChunk = 128;
+cudaError_t launch_decay_chunk(const DecayParams &p, int d, bool sums, cudaStream_t s);
 
 #ifdef __CUDACC__
 // Tokens of request b; -1 for a length outside [0, T].
