@@ -3,24 +3,29 @@
 //
 // Inside a chunk, with b_t = prod_{r<=t} alpha_r, e_s = prod_{r>s} alpha_r, D_ts = prod_{s<r<=t} alpha_r
 // and S the state before the chunk:
-//   o_t = b_t S^T q_t + sum_{s<=t} D_ts (q_t.k_s) v_s        S <- b_C S + sum_s k_s (e_s v_s)^T
+//   o_t = b_t S^T q_t + sum_{s<=t} D_ts (q_t.k_s) v_s        S <- b_C S + sum_s (e_s k_s) v_s^T
 // that is, four products on [token][d] tiles:
-//   scores Q K^T,   O1 = Q S,   O2 = P V with P = D o scores,   dS = K^T (e V)
+//   scores Q K^T,   O = Q S,   P V with P = D o scores,   dS = (e K)^T V
 //
-// The columns of S are independent of each other, so a CTA takes 64 of them for one (request, head):
-// for d = 128 two CTAs share a head, and its q and k tiles meet in L2. S stays in registers (fp32, a row
-// per thread). Everything that is not a bf16 input enters its product as three bf16 terms h + m + l,
-// which carry fp32's 24 significand bits; decays are multiplied up directly, never divided, so a decay
-// of zero or a product that underflows is as exact as any other. Products over a chunk are made in
-// fp64 and rounded once (an error of theirs would repeat in every chunk of a constant decay).
+// A CTA goes along one (request, head), or one segment of it. Q, K and V come by TMA and enter the
+// products as they are. What is not a bf16 input (S, P, e K) enters as three bf16 terms h + m + l, which
+// carry fp32's 24 significand bits: P and (e K)^T from Tensor Memory, as first operands, S from shared
+// memory. S itself stays in registers in fp32 (its sum with b_C S is an ordinary fma; only dS is summed
+// by the tensor cores). Decays are multiplied up, never divided: D_ts is the product of the decays from
+// the end of s's group of 16 tokens, of whole groups and up to t in t's group, so a decay of zero or a
+// product that underflows is as exact as any other. These partial products are made in fp64 and
+// rounded once (an error of theirs would repeat in every chunk of a constant decay).
 //
-// Roles: warps 0-3 turn scores into P (a row per thread, kept in Tensor Memory as the first operand)
-// and write o; warps 4-7 scale V, keep S and write its terms; warp 8 issues the TMA loads, warp 9 the
-// MMAs, warp 10 makes the chunk's decay products. A chunk's products are issued as scores, dS, O1, O2,
-// so that dS of the next chunk needs nothing of the P of this one; K is free after dS, a chunk before
-// Q and V are. Roles meet at mbarriers only, each waited for with a limit; a barrier's next phase
-// needs its waiter's progress, so no wait can miss its phase (those of the TMA warp therefore come in
-// two, for even and odd chunks).
+// Roles: warps 0-7 turn scores into P, add b O and P V and write o (two warps to each 32 rows, on
+// alternate groups of 16 columns of P and halves of O's columns); warps 8-15 keep S and write its terms;
+// warps 16-19 make e K, 16 tokens at a time; warp 20 issues the TMA loads, warp 21 the MMAs, warp 22
+// makes the products of the decays. Products are issued as scores, O, dS, P V: P is made while O and dS
+// run, S's terms for the next chunk while P V and the next scores do. Roles meet at mbarriers only, each
+// waited for with a limit; a barrier's next phase needs its waiter's progress, so no wait can miss its
+// phase.
+//
+// A group of 16 scores (16 fp32 columns of Tensor Memory) is replaced in place by the h and m terms of
+// its 16 entries of P (8 columns each); the l terms have columns of their own.
 #include "../../include/stq.h"
 #include "prefill_common.cuh"
 #include "stq_decay.cuh"
@@ -30,40 +35,48 @@ namespace stq {
 namespace {
 
 constexpr int CT = kDecayChunk;         // tokens of a chunk
-constexpr int NTC = 352;                // threads
+constexpr int NTC = 768;                // threads
 constexpr uint32_t BOX = CT * 128;      // a [128 tokens][64 columns] bf16 box
-// Tensor Memory columns
-constexpr uint32_t TM_SC = 0, TM_O1 = 128, TM_O2 = 192, TM_DS = 256, TM_P = 320;
+// Tensor Memory columns: scores, then P's h and m terms; its l terms; O, then P V; dS; slots of e K's terms
+constexpr uint32_t TM_SC = 0, TM_L = 128, TM_O = 192, TM_DS = 320, TM_KT = 448, KT_COLS = 24;
 
-// Barriers: loads of q, k, v landed; decays made / used by the rows' / by the state's warps; scores done; P made; e V made; dS done / read;
-// terms of S made; O1 done; O2 done; o read; end. Those with 0 and 1 are of even and odd chunks.
-enum { FQ0, FQ1, FK0, FK1, FV0, FV1, GA0, GA1, GF0, GF1, EF, SC, PF, VP, DS0, DS1, DSF, SF, QS0, QS1, OF0, OF1, OFF, END, NBAR };
-
+// Decay products of a chunk, and inside groups of 16 tokens.
 struct ChunkGates {
-    float alpha[CT + 4];  // zeros behind the chunk's
-    float b[CT];
+    float alpha[CT];
+    float b[CT], e[CT];
+    float upto[CT], behind[CT];  // the group's up to the token, and behind it
+    float group[8];
+    double all;
 };
+
+// Loads of q, k, v landed; k free; v free (sums only); gates made / free; scores done; P made; O done /
+// read; P V done / read; e K's slots full / free; dS done / read; S's terms made; end.
+enum { FQ, FK, FV = FK + 3, KE = FV + 3, VE = KE + 3, GA = VE + 3, GF, SC, PF, QS, OS, OF, OFF, KTF, KTE = KTF + 8, DS = KTE + 8, DSF, SF, END, NBAR };
 
 struct ChunkMisc {
     unsigned long long bars[NBAR];
-    alignas(16) ChunkGates g[2];  // of the rows' warps; those of the state's warps follow
-    float e[CT];
-    double all;
+    alignas(16) ChunkGates g;
     uint32_t tmem;
 };
 
-template <int KB>
+template <int KB, int SUMS>
 struct ChunkCfg {
-    static constexpr uint32_t QB = KB * BOX;            // bytes of a q (or k) tile
-    static constexpr uint32_t Q = 0;                    // two stages (of k where only sums are computed)
-    static constexpr uint32_t K = 2 * QB;
-    static constexpr uint32_t V = K + QB;               // two stages
-    static constexpr uint32_t VT = V + 2 * BOX;         // three terms of e V
-    static constexpr uint32_t ST = VT + 3 * BOX;        // three terms of S: [64 KB rows][64 columns]
-    static constexpr uint32_t STB = KB * 64 * 128;
-    static constexpr uint32_t MISC = ST + 3 * STB;
+    static constexpr uint32_t QB = KB * BOX;            // bytes of a q, k or v tile
+    static constexpr int KS = SUMS ? 3 : 1;             // stages of k
+    static constexpr int VS = SUMS ? 3 : 1;             // stages of v
+    static constexpr uint32_t K = 0;
+    static constexpr uint32_t V = K + KS * QB;
+    static constexpr uint32_t Q = V + VS * QB;
+    static constexpr uint32_t ST = Q + (SUMS ? 0 : QB); // three terms of S: [KB][64 KB rows][64 columns]
+    static constexpr uint32_t SA = KB * 64 * 128;       // ... bytes of 64 columns
+    static constexpr uint32_t STB = KB * SA;            // ... of a term
+    static constexpr uint32_t O = ST + (SUMS ? 0 : 3 * STB);  // [32 rows][32 columns] of o for each of 8 warps
+    static constexpr uint32_t MISC = O + (SUMS ? 0 : 8 * 4096);
     static constexpr uint32_t SMEM = MISC + sizeof(ChunkMisc);
     static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
+    static constexpr int SLOTS = SUMS ? 8 : 2;          // of e K
+    static constexpr uint32_t KT = SUMS ? 0 : TM_KT;
+    static constexpr int MAKERS = SUMS ? 3 : 1;         // groups of four warps that make e K
 };
 
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int x, int t, int tile, uint32_t bar)
@@ -97,39 +110,105 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Up to 32 floats (the first n) to a row of o.
-__device__ __forceinline__ void store_o(float *dst, const float (&x)[32], int n, bool wide)
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 {
-#pragma unroll
-    for (int c = 0; c < 32; c += 8) {
-        if (c >= n) return;
-        if (wide) {
-            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + c), "f"(x[c]),
-                         "f"(x[c + 1]), "f"(x[c + 2]), "f"(x[c + 3]), "f"(x[c + 4]), "f"(x[c + 5]), "f"(x[c + 6]),
-                         "f"(x[c + 7])
-                         : "memory");
-        } else {
-            *reinterpret_cast<float4 *>(dst + c) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
-            *reinterpret_cast<float4 *>(dst + c + 4) = make_float4(x[c + 4], x[c + 5], x[c + 6], x[c + 7]);
-        }
-    }
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+                 : "memory");
+}
+
+// Sixteen rows of eight columns: lane l gives rows l / 4 (r[0], r[2]) and l / 4 + 8, columns l % 4 and 4 + l % 4.
+__device__ __forceinline__ void tmem_st_16x8(uint32_t taddr, const uint32_t (&r)[4])
+{
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%4], {%0, %1, %2, %3};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(taddr)
+                 : "memory");
+}
+
+// Four transposed 8 x 8 matrices of 16-bit entries from shared memory.
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap *map, int x, int t, int tile)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(t), "r"(tile)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_store(const CUtensorMap *map, uint32_t src, int x, int t, int tile)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x), "r"(t),
+                 "r"(tile), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// D[tmem] (+)= A[smem] * B[smem], one of several products of the same A in a row: the first (0) leaves A in
+// the tensor core's buffer, the others take it from there, the last (2) lets it go.
+template <int TURN>
+__device__ __forceinline__ void mma_same_a(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    if constexpr (TURN == 0)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16.collector::a::fill [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else if constexpr (TURN == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16.collector::a::use [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16.collector::a::lastuse [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+
+// A thread's registers beyond or below those of the launch, by whole groups of four warps: 256 threads at
+// 96, 256 at 104 and 256 at 40 are the 768 at 80 that the launch has.
+template <int N>
+__device__ __forceinline__ void regs_up()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// One lane of a converged warp; known to the compiler as one (MMAs issued under `lane == 0` took at least
+// 96 cycles each here, under elect 44 to 108).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
 }
 
 template <int KB, int SUMS>
 __global__ void __launch_bounds__(NTC, 1)
-    decay_chunk_kernel(const __grid_constant__ DecayParams p, const int d, const int wide,
-                       const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                       const __grid_constant__ CUtensorMap mv)
+    decay_chunk_kernel(const __grid_constant__ DecayParams p, const int d, const __grid_constant__ CUtensorMap mq,
+                       const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                       const __grid_constant__ CUtensorMap mo)
 {
-    using M = ChunkCfg<KB>;
+    using M = ChunkCfg<KB, SUMS>;
+    constexpr int KS = M::KS, VS = M::VS;
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     ChunkMisc &ms = *reinterpret_cast<ChunkMisc *>(sm + M::MISC);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
-    // (request, head), half of the columns, segment of the prompt
-    const int half = blockIdx.x % KB;
-    const int64_t item = blockIdx.x / KB;
+    // (request, head), segment of the prompt
+    const int64_t item = blockIdx.x;
     const int seg = (int)(item % p.segments);
     const int64_t tile = item / p.segments;
     const int b = (int)(tile / p.H), h = (int)(tile - (int64_t)b * p.H);
@@ -147,19 +226,24 @@ __global__ void __launch_bounds__(NTC, 1)
 
     auto bar = [&](int i) { return smem_u32(&ms.bars[i]); };
     if (tid == 0) {
-        for (int i = 0; i < NBAR; ++i)
-            mbar_init(bar(i), i == PF || i == VP || i == DSF || i == SF || i == OFF ? 128
-                              : i == GA0 || i == GA1                                ? 32
-                              : i == GF0 || i == GF1 || i == EF                     ? 4
-                                                                                    : 1);
+        for (int i = 0; i < NBAR; ++i) {
+            int count = 1;
+            if (i >= KE && i < KE + 3) count = 4 * M::MAKERS;
+            if (i == GF) count = 20;
+            if (i == PF || i == OS || i == OFF || i == DSF || i == SF) count = 8;
+            if (i >= KTF && i < KTF + 8) count = 4;
+            mbar_init(bar(i), count);
+        }
         fence_mbar_init();
     }
-    if (warp == 9) umma::tmem_alloc(smem_u32(&ms.tmem), 512);
+    if (warp == 21) umma::tmem_alloc(smem_u32(&ms.tmem), 512);
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
     const uint32_t tmem = ms.tmem;
-    const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);  // this warp's lanes
+    const int quarter = warp & 3;
+    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);  // this warp's lanes
+    const ChunkGates &g = ms.g;
     // a wait that gave up ends its role; the other roles' waits then give up too
     bool ok = true;
     auto wait = [&](int i, int phase) { return ok = ok && pf::wait_bar(bar(i), (uint32_t)phase & 1u, p.status); };
@@ -170,93 +254,206 @@ __global__ void __launch_bounds__(NTC, 1)
         }
         return ok;
     };
+    auto arrive = [&](int i) {  // of a warp
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(i));
+    };
 
-    if (warp < 4) {
-        // ---- scores -> P; o -----------------------------------------------------------------
-        if constexpr (!SUMS) {
-            const int t = tid;
-            {
-                uint32_t z[16];
+    // Terms of e K, tokens 16 j .. 16 j + 15 of chunk n: a row of Tensor Memory per entry of k, two tokens
+    // to a column, which is how transposed 8 x 8 matrices lie in a warp's registers. Rows of v behind the
+    // prompt's end hold other tokens and are zeroed here, before the MMAs of these tokens.
+    auto make_ek = [&](int n, int j) {
+        const int slot_ = j % M::SLOTS, use = (8 * n + j) / M::SLOTS;
+        if (use > 0 && !wait(KTE + slot_, use - 1)) return;
+        umma::fence_after_sync();
+        const int left = len - (n0 + n) * CT - 16 * j;  // tokens of the group that the prompt has
+        if (quarter < 2 * KB) {
+            const float2 e[2] = {*reinterpret_cast<const float2 *>(&g.e[16 * j + 2 * (lane & 3)]),
+                                 *reinterpret_cast<const float2 *>(&g.e[16 * j + 8 + 2 * (lane & 3)])};
+            const int tok = 16 * j + (lane & 7) + (lane >> 4) * 8, c8 = 4 * (quarter & 1) + (lane >> 3 & 1);
+            const uint32_t k = sb + M::K + (n % KS) * M::QB + (quarter >> 1) * BOX;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) z[i] = 0u;
-                for (int cb = warp + 1; cb < 4; ++cb)  // tokens behind the row's: zero in every chunk
-                    for (int x = 0; x < 3; ++x) tmem_st16(tl + TM_P + 64 * x + 16 * cb, z);
+            for (int x = 0; x < 2; ++x) {  // 16 entries of k
+                uint32_t r[4], hh[4], mm[4], ll[4];
+                ldmatrix4_trans(k + umma::sw128_chunk(tok, c8 + 2 * x), r);
+                if (left < 16)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int u = left - 8 * (i >> 1) - 2 * (lane & 3);
+                        r[i] = u >= 2 ? r[i] : u == 1 ? r[i] & 0xFFFFu : 0u;
+                    }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    pf::split3_pair(__fmul2_rn(make_float2(__uint_as_float(r[i] << 16), __uint_as_float(r[i] & 0xFFFF0000u)),
+                                               e[i >> 1]),
+                                    hh[i], mm[i], ll[i]);
+                const uint32_t to = tl + ((uint32_t)(16 * x) << 16) + M::KT + slot_ * KT_COLS;
+                tmem_st_16x8(to, hh);
+                tmem_st_16x8(to + 8, mm);
+                tmem_st_16x8(to + 16, ll);
             }
-            bool bad = false;
+            tmem_wait_st();
+        }
+        if (left < 16) {
+            if (!wait(FV + n % VS, n / VS)) return;
+            const int u = 4 * quarter + (lane >> 3);  // four rows of a warp
+            if (u >= left)
+                for (int x = 0; x < KB; ++x)
+                    *reinterpret_cast<uint4 *>(sm + M::V + (n % VS) * M::QB + x * BOX + umma::sw128_chunk(16 * j + u, lane & 7)) =
+                        make_uint4(0u, 0u, 0u, 0u);
+            umma::fence_proxy_async();
+        }
+        umma::fence_before_sync();
+        arrive(KTF + slot_);
+    };
+    // ... of every chunk, by group `who` of the makers
+    auto make_all = [&](int who) {
+        for (int n = 0; n < N; ++n) {
+            if (!wait(GA, n) || !wait(FK + n % KS, n / KS)) break;
+            for (int j = who; j < 8 && ok; j += M::MAKERS) make_ek(n, j);
+            if (!ok) break;
+            arrive(KE + n % KS);
+            arrive(GF);
+        }
+    };
+
+    if (warp < 8) {
+        regs_up<96>();
+        // ---- P, o -----------------------------------------------------------------------------
+        if constexpr (SUMS) {
+            make_all(warp >> 2);
+        } else {
+            const int t = 32 * quarter + lane, sub = warp >> 2, l16 = lane & 15, top = 2 * quarter + 1;
+            const bool hi = lane >= 16;
+            const uint32_t z[16] = {}, z8[8] = {};
+            for (int c = top + 1 + sub; c < 8; c += 2)  // tokens behind the row's: zero in every chunk
+                tmem_st8(tl + TM_L + 8 * c, z8);
+            float2 bad = make_float2(0.f, 0.f);  // 0 x is not 0 for an x that is not finite
             for (int n = 0; n < N; ++n) {
-                const int t0 = (n0 + n) * CT, st = n & 1;
-                if (!wait(GA0 + st, n >> 1)) break;
-                const ChunkGates &g = ms.g[st];
-                const float bt = g.b[t];
+                const int t0 = (n0 + n) * CT;
+                if (!wait(GA, n)) break;
+                const float bt = g.b[t], upto = g.upto[t];
                 if (!wait(SC, n)) break;
                 umma::fence_after_sync();
-                float D = 0.f;
-#pragma unroll 1
-                for (int cb = warp; cb >= 0; --cb) {
-                    float v[32];
-                    umma::tmem_ld32(tl + TM_SC + 32 * cb, v);
-                    uint32_t hh[16], mm[16], ll[16];
-                    const bool diag = cb == warp;
-                    float right = g.alpha[32 * cb + 32];  // the decay of the token right of the group of four
+                for (int c = top + 1 + sub; c < 8; c += 2) tmem_st16(tl + TM_SC + 16 * c, z);
+                // The topmost group: of the two halves of the rows one has its diagonal there. The other has
+                // nothing (sub 0), or all of the group below its own (sub 1).
+                int c = top - sub;
+                {
+                    float v[16], D = 0.f, x[16];
+                    pf::tmem_ld16(tl + TM_SC + 16 * c, v);
+                    const bool diag = hi == (sub == 0);
 #pragma unroll
-                    for (int e = 28; e >= 0; e -= 4) {
-                        const float4 al = *reinterpret_cast<const float4 *>(&g.alpha[32 * cb + e]);
-                        const float next[4] = {al.y, al.z, al.w, right};
-                        right = al.x;
-                        float x[4];
-#pragma unroll
-                        for (int i = 3; i >= 0; --i) {
-                            D *= next[i];
-                            if (diag && e + i >= lane) D = e + i == lane ? 1.f : 0.f;
-                            x[i] = diag && e + i > lane ? 0.f : v[e + i] * D;
-                        }
-                        pf::split3_pair(make_float2(x[0], x[1]), hh[e / 2], mm[e / 2], ll[e / 2]);
-                        pf::split3_pair(make_float2(x[2], x[3]), hh[e / 2 + 1], mm[e / 2 + 1], ll[e / 2 + 1]);
+                    for (int i = 15; i >= 0; --i) {
+                        if (i < 15) D *= g.alpha[16 * c + i + 1];
+                        if (i >= l16) D = 1.f;
+                        const float w = diag ? D : g.behind[16 * c + i] * upto;
+                        x[i] = (diag ? i > l16 : sub == 0) ? 0.f : v[i] * w;
                     }
-                    tmem_st16(tl + TM_P + 16 * cb, hh);
-                    tmem_st16(tl + TM_P + 64 + 16 * cb, mm);
-                    tmem_st16(tl + TM_P + 128 + 16 * cb, ll);
+                    uint32_t hm[16], ll[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) pf::split3_pair(make_float2(x[2 * i], x[2 * i + 1]), hm[i], hm[8 + i], ll[i]);
+                    tmem_st16(tl + TM_SC + 16 * c, hm);
+                    tmem_st8(tl + TM_L + 8 * c, ll);
+                }
+                float w = hi ? upto * g.group[top - 1] : upto;
+                if (sub && quarter) w *= g.group[top - 2];
+#pragma unroll 1
+                for (c -= 2; c >= 0; c -= 2) {
+                    float v[16];
+                    pf::tmem_ld16(tl + TM_SC + 16 * c, v);
+                    uint32_t hm[16], ll[8];
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(&g.behind[16 * c + i]);
+                        const float2 w2 = make_float2(w, w);
+                        pf::split3_pair(__fmul2_rn(make_float2(v[i], v[i + 1]), __fmul2_rn(make_float2(f.x, f.y), w2)),
+                                        hm[i / 2], hm[8 + i / 2], ll[i / 2]);
+                        pf::split3_pair(__fmul2_rn(make_float2(v[i + 2], v[i + 3]), __fmul2_rn(make_float2(f.z, f.w), w2)),
+                                        hm[i / 2 + 1], hm[8 + i / 2 + 1], ll[i / 2 + 1]);
+                    }
+                    tmem_st16(tl + TM_SC + 16 * c, hm);
+                    tmem_st8(tl + TM_L + 8 * c, ll);
+                    if (c >= 2) w *= g.group[c] * g.group[c - 1];
                 }
                 tmem_wait_st();
                 umma::fence_before_sync();
-                mbar_arrive(bar(PF));
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(GF0 + st));
+                arrive(PF);
+                arrive(GF);
 
-                if (!wait(OF0 + st, n >> 1)) break;
+                if (!wait(QS, n)) break;
                 umma::fence_after_sync();
-                float *dst = p.o + (tile * p.T + t0 + t) * d + 64 * half;
-                const bool live = t0 + t < len;
+                const int c0 = 32 * KB * sub;
+                float o1[32 * KB];
 #pragma unroll
-                for (int c = 0; c < 64; c += 32) {
-                    float x[32], y[32];
-                    umma::tmem_ld32(tl + TM_O1 + c, x);
-                    umma::tmem_ld32(tl + TM_O2 + c, y);
-                    if (c == 32) {
+                for (int cc = 0; cc < 32 * KB; cc += 16) {
+                    float x[16];
+                    pf::tmem_ld16(tl + TM_O + c0 + cc, x);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o1[cc + i] = x[i];
+                }
+                umma::fence_before_sync();
+                arrive(OS);
+
+                if (!wait(OF, n)) break;
+                umma::fence_after_sync();
+                const bool whole = t0 + 32 * quarter + 32 <= len;  // every row of the warp is the prompt's
+#pragma unroll
+                for (int cc = 0; cc < 32 * KB; cc += 16) {
+                    const int to = c0 + cc;
+                    float x[16];
+                    pf::tmem_ld16(tl + TM_O + to, x);
+                    if (cc + 16 == 32 * KB) {
                         umma::fence_before_sync();
-                        mbar_arrive(bar(OFF));
+                        arrive(OFF);
                     }
+                    if ((cc & 31) == 0) {  // the tile's last use is over
+                        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        __syncwarp();
+                    }
+                    if (to >= d) continue;
+                    float2 y[8];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        x[e] = fmaf(bt, x[e], y[e]);
-                        bad |= live && c + e < d && !(fabsf(x[e]) <= 3.402823466e38f);
+                    for (int i = 0; i < 8; ++i) {
+                        y[i] = __ffma2_rn(make_float2(bt, bt), make_float2(o1[cc + 2 * i], o1[cc + 2 * i + 1]),
+                                          make_float2(x[2 * i], x[2 * i + 1]));
+                        if (t0 + t < len) bad = __ffma2_rn(y[i], make_float2(0.f, 0.f), bad);
                     }
-                    if (live) store_o(dst + c, x, d - c, wide);
+                    if (whole) {
+                        uint8_t *tile_o = sm + M::O + warp * 4096;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            *reinterpret_cast<float4 *>(tile_o + umma::sw128_chunk(lane, (cc & 31) / 4 + i)) =
+                                make_float4(y[2 * i].x, y[2 * i].y, y[2 * i + 1].x, y[2 * i + 1].y);
+                        if ((cc & 31) == 16 || to + 16 == d) {
+                            umma::fence_proxy_async();
+                            __syncwarp();
+                            if (lane == 0) tma_store(&mo, sb + M::O + warp * 4096, to & ~31, t0 + 32 * quarter, (int)tile);
+                        }
+                    } else if (t0 + t < len) {
+                        float *dst = p.o + (tile * p.T + t0 + t) * d + to;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            *reinterpret_cast<float4 *>(dst + 4 * i) = make_float4(y[2 * i].x, y[2 * i].y, y[2 * i + 1].x, y[2 * i + 1].y);
+                    }
                 }
             }
-            if (bad) flag(p.status, kFlagNonfinite);
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+            if (!(bad.x + bad.y == 0.f)) flag(p.status, kFlagNonfinite);
         }
-    } else if (warp < 8) {
-        // ---- e V, S -------------------------------------------------------------------------
-        const int i = tid - 128;  // token of the chunk; row of S
-        const int cols = i < d ? min(64, d) : 0;
-        float *record = p.records ? p.records + ((tile * p.segments + seg) * d + i) * d + 64 * half : nullptr;
-        float *pool = p.states + (((int64_t)slot * p.H + h) * d + i) * d + 64 * half;
-        float S[64];
+    } else if (warp < 16) {
+        regs_up<104>();
+        // ---- S ----------------------------------------------------------------------------------
+        constexpr int SC_ = 32 * KB;  // columns of a thread
+        const int i = 32 * quarter + lane, c0 = SC_ * (warp >> 2 & 1);
+        const int cols = i < d ? min(SC_, d - c0) : 0;
+        float *record = p.records ? p.records + ((tile * p.segments + seg) * d + i) * d + c0 : nullptr;
+        float *pool = p.states + (((int64_t)slot * p.H + h) * d + i) * d + c0;
+        float S[SC_];
         {
             const float *from = p.segments > 1 ? record : pool;
 #pragma unroll
-            for (int c = 0; c < 64; c += 4) {
+            for (int c = 0; c < SC_; c += 4) {
                 const float4 x = !SUMS && c < cols ? *reinterpret_cast<const float4 *>(from + c) : make_float4(0.f, 0.f, 0.f, 0.f);
                 S[c] = x.x;
                 S[c + 1] = x.y;
@@ -265,181 +462,164 @@ __global__ void __launch_bounds__(NTC, 1)
             }
         }
         auto put_state = [&]() {
-            if (i < 64 * KB)
+            if (quarter < 2 * KB) {
+                uint8_t *st = sm + M::ST + (c0 >> 6) * M::SA;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
+                for (int c = 0; c < SC_ / 8; ++c) {
                     float x[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] = S[8 * c + e];
-                    pf::store_split3(sm + M::ST, sm + M::ST + M::STB, sm + M::ST + 2 * M::STB, umma::sw128_chunk(i, c), x);
+                    pf::store_split3(st, st + M::STB, st + 2 * M::STB, umma::sw128_chunk(i, (c0 >> 3 & 7) + c), x);
                 }
-            umma::fence_proxy_async();
-            mbar_arrive(bar(SF));
-        };
-        double all = 1.0;   // the chunk's product
-        double upto = 1.0;  // the segment's
-        auto scale_v = [&](int n) {
-            const int t0 = (n0 + n) * CT, st = n & 1;
-            if (!wait(GA0 + st, n >> 1)) return;
-            const float ef = ms.e[i];
-            all = ms.all;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(EF));
-            if (!wait(FV0 + st, n >> 1)) return;
-            uint8_t *vt = sm + M::VT, *v = sm + M::V + st * BOX;
-            const bool live = i < len - t0;
-            if (len - t0 < CT) {
-                // rows behind the prompt's end hold other tokens: zero, also in the tiles the MMAs read
-                if (!wait(SUMS ? FK0 + st : FK0, SUMS ? n >> 1 : n)) return;
-                uint8_t *k = sm + (SUMS ? M::Q + st * M::QB : M::K);
-                if (!live)
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        *reinterpret_cast<uint4 *>(v + umma::sw128_chunk(i, c)) = make_uint4(0u, 0u, 0u, 0u);
-                        for (int x = 0; x < KB; ++x)
-                            *reinterpret_cast<uint4 *>(k + x * BOX + umma::sw128_chunk(i, c)) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-            }
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const uint32_t off = umma::sw128_chunk(i, c);
-                float x[8];
-                pf::bf16x8_to_f32(*reinterpret_cast<const uint4 *>(v + off), x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = live ? x[e] * ef : 0.f;
-                pf::store_split3(vt, vt + BOX, vt + 2 * BOX, off, x);
             }
             umma::fence_proxy_async();
-            mbar_arrive(bar(VP));
+            arrive(SF);
         };
+        double upto = 1.0;  // the segment's decay
         if (!SUMS) put_state();
-        scale_v(0);
         for (int n = 0; n < N && ok; ++n) {
-            const float bc = (float)all;
-            upto *= all;
-            if (!wait(DS0 + (n & 1), n >> 1)) break;
+            if (!wait(GA, n)) break;
+            const float bc = (float)g.all;
+            upto *= g.all;
+            arrive(GF);
+            if (!wait(DS, n)) break;
             umma::fence_after_sync();
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float x[32];
-                umma::tmem_ld32(tl + TM_DS + 32 * c, x);
+            for (int c = 0; c < SC_; c += 16) {
+                float x[16];
+                pf::tmem_ld16(tl + TM_DS + c0 + c, x);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) S[32 * c + e] = fmaf(bc, S[32 * c + e], x[e]);
+                for (int e = 0; e < 16; ++e) S[c + e] = fmaf(bc, S[c + e], x[e]);
             }
             umma::fence_before_sync();
-            mbar_arrive(bar(DSF));
-            if (n + 1 == N) break;
-            scale_v(n + 1);
-            if (!SUMS) {
-                if (!wait(QS0 + (n & 1), n >> 1)) break;
-                put_state();
-            }
+            arrive(DSF);
+            if (!SUMS && n + 1 < N) put_state();  // O of this chunk was done before dS
         }
         if (ok && (SUMS || last)) {
             float *to = SUMS ? record : pool;
             bool bad = false;
 #pragma unroll
-            for (int c = 0; c < 64; c += 4)
+            for (int c = 0; c < SC_; c += 4)
                 if (c < cols) {
                     *reinterpret_cast<float4 *>(to + c) = make_float4(S[c], S[c + 1], S[c + 2], S[c + 3]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) bad |= !(fabsf(S[c + e]) <= 3.402823466e38f);
                 }
             if (bad) flag(p.status, kFlagNonfinite);
-            if (SUMS && i == 0 && half == 0) p.products[tile * p.segments + seg] = (float)upto;
+            if (SUMS && tid == 256) p.products[tile * p.segments + seg] = (float)upto;
         }
-    } else if (warp == 8) {
+    } else if (warp < 20) {
+        regs_down<40>();
+        // ---- e K ----------------------------------------------------------------------------
+        make_all(M::MAKERS - 1);
+    } else if (regs_down<40>(); warp == 20) {
         // ---- TMA ----------------------------------------------------------------------------
-        if (lane == 0) {
-            int nq[2] = {0, 0}, nk[2] = {0, 0}, nv[2] = {0, 0};  // loads issued on each barrier
+        if (elect_one()) {
+            auto load = [&](uint32_t to, const CUtensorMap *map, int n, int full) {
+                mbar_arrive_expect_tx(bar(full), M::QB);
+                for (int x = 0; x < KB; ++x)
+                    tma_box(sb + to + x * BOX, map, 64 * x, (n0 + n) * CT, (int)tile, bar(full));
+            };
+            int nq = 0, nk = 0, nv = 0;  // loads issued
             for (int n = 0; n < N; ++n) {
-                const int t0 = (n0 + n) * CT, st = n & 1;
+                if (n + 1 < N)  // the next chunk to L2: the loads below start late
+                    for (int x = 0; x < KB; ++x) {
+                        const int t = (n0 + n + 1) * CT;
+                        tma_prefetch(&mk, 64 * x, t, (int)tile);
+                        if (!SUMS) tma_prefetch(&mq, 64 * x, t, (int)tile);
+                        tma_prefetch(&mv, 64 * x, t, (int)tile);
+                    }
                 if constexpr (SUMS) {
-                    if (n >= 2 && !once(DS0 + st, (n - 2) >> 1)) break;
-                    mbar_arrive_expect_tx(bar(FK0 + st), M::QB);
-                    for (int x = 0; x < KB; ++x)
-                        tma_box(sb + M::Q + st * M::QB + x * BOX, &mk, 64 * x, t0, (int)tile, bar(FK0 + st));
-                    ++nk[st];
+                    if (n >= KS && !once(KE + n % KS, n / KS - 1)) break;
+                    load(M::K + n % KS * M::QB, &mk, n, FK + n % KS);
+                    ++nk;
+                    if (n >= VS && !once(VE + n % VS, n / VS - 1)) break;
                 } else {
-                    if (n >= 2 && !once(QS0 + st, (n - 2) >> 1)) break;
-                    mbar_arrive_expect_tx(bar(FQ0 + st), M::QB);
-                    for (int x = 0; x < KB; ++x)
-                        tma_box(sb + M::Q + st * M::QB + x * BOX, &mq, 64 * x, t0, (int)tile, bar(FQ0 + st));
-                    ++nq[st];
-                    if (n >= 1 && !once(DS0 + (st ^ 1), (n - 1) >> 1)) break;
-                    mbar_arrive_expect_tx(bar(FK0), M::QB);
-                    for (int x = 0; x < KB; ++x) tma_box(sb + M::K + x * BOX, &mk, 64 * x, t0, (int)tile, bar(FK0));
-                    ++nk[0];
-                    if (n >= 2 && !once(OF0 + st, (n - 2) >> 1)) break;
+                    if (n >= 1 && !once(QS, n - 1)) break;  // the scores were done before O
+                    load(M::Q, &mq, n, FQ);
+                    ++nq;
+                    if (n >= 1 && !once(KE, n - 1)) break;
+                    load(M::K, &mk, n, FK);
+                    ++nk;
+                    if (n >= 1 && !once(OF, n - 1)) break;
                 }
-                mbar_arrive_expect_tx(bar(FV0 + st), BOX);
-                tma_box(sb + M::V + st * BOX, &mv, 64 * half, t0, (int)tile, bar(FV0 + st));
-                ++nv[st];
+                load(M::V + n % VS * M::QB, &mv, n, FV + n % VS);
+                ++nv;
             }
             // no copy is in flight when the CTA ends, also where a wait gave up
-            for (int st = 0; st < 2; ++st) {
-                if (nq[st]) mbar_wait_bounded(bar(FQ0 + st), (uint32_t)(nq[st] - 1) & 1u);
-                if (nk[st]) mbar_wait_bounded(bar(FK0 + st), (uint32_t)(nk[st] - 1) & 1u);
-                if (nv[st]) mbar_wait_bounded(bar(FV0 + st), (uint32_t)(nv[st] - 1) & 1u);
-            }
+            if (nq) mbar_wait_bounded(bar(FQ), (uint32_t)(nq - 1) & 1u);
+            for (int n = nk - KS < 0 ? 0 : nk - KS; n < nk; ++n) mbar_wait_bounded(bar(FK + n % KS), (uint32_t)(n / KS) & 1u);
+            for (int n = nv - VS < 0 ? 0 : nv - VS; n < nv; ++n) mbar_wait_bounded(bar(FV + n % VS), (uint32_t)(n / VS) & 1u);
         }
-    } else if (warp == 9) {
+    } else if (warp == 21) {
         // ---- MMA ----------------------------------------------------------------------------
-        if (lane == 0) {
-            constexpr uint32_t ID_SC = umma::idesc_bf16(128, 128, 0, 0), ID_DS = umma::idesc_bf16(128, 64, 1, 1),
-                               ID_O = umma::idesc_bf16(128, 64, 0, 1);
+        if (elect_one()) {
+            const uint32_t cols = KB == 2 ? 128 : d;  // of v
+            const int steps = KB == 2 ? 8 : d / 16;   // of 16 entries of q and k
+            const uint32_t id_sc = umma::idesc_bf16(128, 128, 0, 0), id_d = umma::idesc_bf16(128, 0, 0, 1) | (cols >> 3) << 17;
+            uint64_t dq = umma::smem_desc(sb + M::Q, 16, 1024), dk = umma::smem_desc(sb + M::K, 16, 1024),
+                           dv = umma::smem_desc(sb + M::V, BOX, 1024), ds = umma::smem_desc(sb + M::ST, M::SA, 1024);
             for (int n = 0; n < N; ++n) {
-                const int st = n & 1;
-                const uint32_t q = sb + M::Q + st * M::QB, k = SUMS ? q : sb + M::K, v = sb + M::V + st * BOX;
-                if (!once(SUMS ? FK0 + st : FK0, SUMS ? n >> 1 : n)) break;
+                // (kept from making all tiles' descriptors before the loop, which is more than its registers)
+                asm volatile("" : "+l"(dq), "+l"(dk), "+l"(dv), "+l"(ds));
+                const uint64_t kn = dk + n % KS * (M::QB >> 4), vn = dv + n % VS * (M::QB >> 4);
                 if constexpr (!SUMS) {
-                    if (!once(FQ0 + st, n >> 1)) break;
-                    umma::fence_after_sync();  // the scores before were read: PF was waited for
+                    // P of the chunk before is used up when its P V is done
+                    if (!once(FK + n % KS, n / KS) || !once(FQ, n) || (n > 0 && !once(OF, n - 1))) break;
+                    umma::fence_after_sync();
 #pragma unroll
                     for (int kk = 0; kk < 4 * KB; ++kk)
-                        umma::mma_bf16(tmem + TM_SC, umma::smem_desc(q + (kk >> 2) * BOX + (kk & 3) * 32, 16, 1024),
-                                       umma::smem_desc(k + (kk >> 2) * BOX + (kk & 3) * 32, 16, 1024), ID_SC, kk != 0);
+                        if (kk < steps)
+                            umma::mma_bf16(tmem + TM_SC, dq + (((kk >> 2) * BOX + (kk & 3) * 32) >> 4),
+                                           kn + (((kk >> 2) * BOX + (kk & 3) * 32) >> 4), id_sc, kk != 0);
                     umma::mma_commit(bar(SC));
-                }
-                if (!once(VP, n)) break;
-                if (n > 0 && !once(DSF, n - 1)) break;
-                umma::fence_after_sync();
-                // rows 64.. of dS are not read where d <= 64 (the tile behind k stands in for their k)
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-#pragma unroll
-                    for (int x = 0; x < 3; ++x)
-                        umma::mma_bf16(tmem + TM_DS, umma::smem_desc(k + kk * 2048, BOX, 1024),
-                                       umma::smem_desc(sb + M::VT + x * BOX + kk * 2048, 16, 1024), ID_DS, (kk | x) != 0);
-                umma::mma_commit(bar(DS0 + st));
-                if constexpr (!SUMS) {
-                    if (!once(SF, n)) break;
-                    if (n > 0 && !once(OFF, n - 1)) break;
+                    if (!once(SF, n) || (n > 0 && !once(OFF, n - 1))) break;
                     umma::fence_after_sync();
 #pragma unroll
                     for (int kk = 0; kk < 4 * KB; ++kk)
-#pragma unroll
-                        for (int x = 0; x < 3; ++x)
-                            umma::mma_bf16(tmem + TM_O1, umma::smem_desc(q + (kk >> 2) * BOX + (kk & 3) * 32, 16, 1024),
-                                           umma::smem_desc(sb + M::ST + x * M::STB + kk * 2048, 16, 1024), ID_O, (kk | x) != 0);
-                    umma::mma_commit(bar(QS0 + st));
-                    if (!once(PF, n)) break;
+                        if (kk < steps) {
+                            const uint64_t a = dq + (((kk >> 2) * BOX + (kk & 3) * 32) >> 4), s = ds + (kk * 2048 >> 4);
+                            mma_same_a<0>(tmem + TM_O, a, s + (2 * M::STB >> 4), id_d, kk != 0);
+                            mma_same_a<1>(tmem + TM_O, a, s + (M::STB >> 4), id_d, 1);
+                            mma_same_a<2>(tmem + TM_O, a, s, id_d, 1);
+                        }
+                    umma::mma_commit(bar(QS));
+                }
+                if (!once(FV + n % VS, n / VS) || (n > 0 && !once(DSF, n - 1))) break;
+                // rows d.. of dS are not read
+#pragma unroll 1
+                for (int j = 0; j < 8; ++j) {
+                    const int slot_ = j % M::SLOTS, use = (8 * n + j) / M::SLOTS;
+                    if (!once(KTF + slot_, use)) break;
+                    umma::fence_after_sync();
+                    const uint32_t a = tmem + M::KT + slot_ * KT_COLS;
+                    const uint64_t v = vn + j * (2048 >> 4);
+                    mma_ts(tmem + TM_DS, a + 16, v, id_d, j != 0);
+                    mma_ts(tmem + TM_DS, a + 8, v, id_d, 1);
+                    mma_ts(tmem + TM_DS, a, v, id_d, 1);
+                    umma::mma_commit(bar(KTE + slot_));
+                }
+                if (!ok) break;
+                umma::mma_commit(bar(DS));
+                if constexpr (SUMS) {
+                    umma::mma_commit(bar(VE + n % VS));
+                } else {
+                    if (!once(PF, n) || !once(OS, n)) break;
                     umma::fence_after_sync();
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
+                    for (int kk = 0; kk < 8; ++kk) mma_ts(tmem + TM_O, tmem + TM_L + 8 * kk, vn + (kk * 2048 >> 4), id_d, kk != 0);
 #pragma unroll
-                        for (int x = 0; x < 3; ++x)
-                            mma_ts(tmem + TM_O2, tmem + TM_P + 64 * x + 8 * kk, umma::smem_desc(v + kk * 2048, 16, 1024),
-                                   ID_O, (kk | x) != 0);
-                    umma::mma_commit(bar(OF0 + st));
+                    for (int kk = 0; kk < 16; ++kk)
+                        mma_ts(tmem + TM_O, tmem + TM_SC + 16 * (kk & 7) + (kk < 8 ? 8 : 0), vn + ((kk & 7) * 2048 >> 4), id_d, 1);
+                    umma::mma_commit(bar(OF));
                 }
             }
             // what was issued is over before Tensor Memory is given back, also where a wait gave up
             umma::mma_commit(bar(END));
             mbar_wait_bounded(bar(END), 0);
         }
-    } else {
-        // ---- products of the decays -----------------------------------------------------------
+    } else if (warp == 22) {
+        // ---- products of the decays: four tokens to a lane, four lanes to a group ----------------
         const float *alpha = p.alpha + tile * p.T;
         float next[4];
         auto load = [&](int n) {
@@ -447,65 +627,88 @@ __global__ void __launch_bounds__(NTC, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) next[i] = n < N && i < len - t ? alpha[t + i] : 1.f;
         };
-        if (lane < 4) ms.g[0].alpha[CT + lane] = ms.g[1].alpha[CT + lane] = 0.f;
         load(0);
         for (int n = 0; n < N; ++n) {
-            const int st = n & 1;
             const float a[4] = {next[0], next[1], next[2], next[3]};
             load(n + 1);
-            const double p1 = (double)a[0] * a[1], p2 = p1 * a[2], p3 = p2 * a[3];
-            const double s2 = a[3], s1 = s2 * a[2], s0 = s1 * a[1];
-            double pre = p3, suf = p3;  // inclusive over the lanes from the left and from the right
+            double pre = (double)a[0] * a[1] * a[2] * a[3], suf = pre;
+            // inclusive over the group's lanes, from the left and from the right
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, pre, o), z = __shfl_down_sync(0xffffffffu, suf, o);
-                if (lane >= o) pre *= y;
-                if (lane + o < 32) suf *= z;
+            for (int o = 1; o < 4; o <<= 1) {
+                const double y = __shfl_up_sync(0xffffffffu, pre, o, 4), z = __shfl_down_sync(0xffffffffu, suf, o, 4);
+                if ((lane & 3) >= o) pre *= y;
+                if ((lane & 3) + o < 4) suf *= z;
             }
-            const double all = __shfl_sync(0xffffffffu, pre, 31);
-            pre = __shfl_up_sync(0xffffffffu, pre, 1);
-            suf = __shfl_down_sync(0xffffffffu, suf, 1);
-            if (lane == 0) pre = 1.0;
-            if (lane == 31) suf = 1.0;
-            if (!SUMS && n >= 2 && !wait(GF0 + st, (n - 2) >> 1)) break;
-            if (n >= 1 && !wait(EF, n - 1)) break;
-            ChunkGates &g = ms.g[st];
-            *reinterpret_cast<float4 *>(&g.alpha[4 * lane]) = make_float4(a[0], a[1], a[2], a[3]);
-            *reinterpret_cast<float4 *>(&g.b[4 * lane]) =
-                make_float4((float)(pre * a[0]), (float)(pre * p1), (float)(pre * p2), (float)(pre * p3));
-            *reinterpret_cast<float4 *>(&ms.e[4 * lane]) =
-                make_float4((float)(suf * s0), (float)(suf * s1), (float)(suf * s2), (float)suf);
-            if (lane == 0) ms.all = all;
-            mbar_arrive(bar(GA0 + st));
+            const double group = __shfl_sync(0xffffffffu, pre, 3, 4);
+            pre = __shfl_up_sync(0xffffffffu, pre, 1, 4);
+            suf = __shfl_down_sync(0xffffffffu, suf, 1, 4);
+            if ((lane & 3) == 0) pre = 1.0;
+            if ((lane & 3) == 3) suf = 1.0;
+            // the same over the groups
+            double left = group, right = group;
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+                const double y = __shfl_up_sync(0xffffffffu, left, o), z = __shfl_down_sync(0xffffffffu, right, o);
+                if (lane >= o) left *= y;
+                if (lane + o < 32) right *= z;
+            }
+            const double all = __shfl_sync(0xffffffffu, left, 31);
+            left = __shfl_up_sync(0xffffffffu, left, 4);
+            right = __shfl_down_sync(0xffffffffu, right, 4);
+            if (lane < 4) left = 1.0;
+            if (lane >= 28) right = 1.0;
+            if (n >= 1 && !wait(GF, n - 1)) break;
+            ChunkGates &to = ms.g;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                pre *= a[i];
+                to.alpha[4 * lane + i] = a[i];
+                to.upto[4 * lane + i] = (float)pre;
+                to.b[4 * lane + i] = (float)(left * pre);
+            }
+#pragma unroll
+            for (int i = 3; i >= 0; --i) {
+                to.behind[4 * lane + i] = (float)suf;
+                to.e[4 * lane + i] = (float)(suf * right);
+                suf *= a[i];
+            }
+            if ((lane & 3) == 0) to.group[lane >> 2] = (float)group;
+            if (lane == 0) to.all = all;
+            arrive(GA);
         }
     }
     __syncwarp();
     __syncthreads();
-    if (warp == 9) umma::tmem_dealloc(tmem, 512);
+    if (warp == 21) umma::tmem_dealloc(tmem, 512);
 }
 
 template <int KB, int SUMS>
 cudaError_t launch(const DecayParams &p, int d, cudaStream_t s)
 {
     const EncodeTiled enc = encode_tiled();
-    CUtensorMap map[3];
-    const void *in[3] = {p.q, p.k, p.v};
-    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)p.T, (cuuint64_t)p.B * p.H};
-    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)d * 2 * p.T};
-    const cuuint32_t box[3] = {64, CT, 1}, estr[3] = {1, 1, 1};
-    for (int i = 0; i < 3; ++i)
-        if (!enc || enc(&map[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(in[i]), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    if (!enc) return cudaErrorNotSupported;
+    // q, k, v as boxes of 128 tokens x 64 columns, o as boxes of 32 x 32; what lies outside is read as zeros
+    // and not written
+    CUtensorMap map[4];
+    const void *at[4] = {p.q, p.k, p.v, p.o};
+    for (int i = 0; i < 4; ++i) {
+        const cuuint64_t size = i < 3 ? 2 : 4, row = (cuuint64_t)d * size;
+        const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)p.T, (cuuint64_t)p.B * p.H};
+        const cuuint64_t strides[2] = {row, row * p.T};
+        const cuuint32_t box[3] = {i < 3 ? 64u : 32u, i < 3 ? (cuuint32_t)CT : 32u, 1}, estr[3] = {1, 1, 1};
+        if (enc(&map[i], i < 3 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
+                const_cast<void *>(at[i]), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorNotSupported;
+    }
     auto kernel = decay_chunk_kernel<KB, SUMS>;
     const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ChunkCfg<KB>::SMEM);
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ChunkCfg<KB, SUMS>::SMEM);
     if (e != cudaSuccess) return e;
-    const int64_t grid = (int64_t)p.B * p.H * p.segments * KB;
+    const int64_t grid = (int64_t)p.B * p.H * p.segments;
     if (grid > 0x7fffffff) return cudaErrorNotSupported;
-    const int wide = reinterpret_cast<uintptr_t>(p.o) % 32 == 0;
-    kernel<<<(unsigned)grid, NTC, ChunkCfg<KB>::SMEM, s>>>(p, d, wide, map[0], map[1], map[2]);
+    kernel<<<(unsigned)grid, NTC, ChunkCfg<KB, SUMS>::SMEM, s>>>(p, d, map[0], map[1], map[2], map[3]);
     return cudaGetLastError();
 }
 

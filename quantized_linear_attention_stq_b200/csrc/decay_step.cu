@@ -284,7 +284,7 @@ Split split(int B, int H, int T, int d, int in_bf16, bool cut)
     if (r.chunk) {
         // one CTA to an SM: rounds of CTAs times chunks of each, the first pass at 2/5 of the main
         // one, the two launches more at three chunks
-        const int64_t chunks = ((int64_t)T + kDecayChunk - 1) / kDecayChunk, ctas = tiles * (d > 64 ? 2 : 1);
+        const int64_t chunks = ((int64_t)T + kDecayChunk - 1) / kDecayChunk, ctas = tiles;
         double best = 0.0;
         int64_t per = chunks;
         for (int64_t n = 1; n <= (cut ? 64 : 1) && n <= chunks; ++n) {

@@ -96,17 +96,24 @@ __device__ __forceinline__ void store_codes_row(uint8_t *gblock, int i, int part
 // ---------------------------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t bf2_bits(__nv_bfloat162 h) { return *reinterpret_cast<uint32_t *>(&h); }
 
-// x = h + m + l exactly (three bf16 terms carry the 24 significand bits of each value).
+// x = h + m + l exactly (three bf16 terms carry the 24 significand bits of each value). The remainders
+// come from the fma that takes bf16 factors: with the terms unpacked to fp32 first a pair took 17 issue
+// cycles here, so it takes 10.
 __device__ __forceinline__ void split3_pair(float2 x, uint32_t &h, uint32_t &m, uint32_t &l)
 {
-    const float2 neg = make_float2(-1.f, -1.f);
-    const __nv_bfloat162 hb = __floats2bfloat162_rn(x.x, x.y);
-    const float2 r1 = __ffma2_rn(__bfloat1622float2(hb), neg, x);
-    const __nv_bfloat162 mb = __floats2bfloat162_rn(r1.x, r1.y);
-    const float2 r2 = __ffma2_rn(__bfloat1622float2(mb), neg, r1);
-    h = bf2_bits(hb);
-    m = bf2_bits(mb);
-    l = bf2_bits(__floats2bfloat162_rn(r2.x, r2.y));
+    asm("{\n\t.reg .b16 lo, hi, neg;\n\t.reg .f32 a, b;\n\t"
+        "mov.b16 neg, 0xBF80;\n\t"  // -1
+        "cvt.rn.bf16x2.f32 %0, %4, %3;\n\t"
+        "mov.b32 {lo, hi}, %0;\n\t"
+        "fma.rn.f32.bf16 a, lo, neg, %3;\n\t"
+        "fma.rn.f32.bf16 b, hi, neg, %4;\n\t"
+        "cvt.rn.bf16x2.f32 %1, b, a;\n\t"
+        "mov.b32 {lo, hi}, %1;\n\t"
+        "fma.rn.f32.bf16 a, lo, neg, a;\n\t"
+        "fma.rn.f32.bf16 b, hi, neg, b;\n\t"
+        "cvt.rn.bf16x2.f32 %2, b, a;\n\t}"
+        : "=&r"(h), "=&r"(m), "=&r"(l)
+        : "f"(x.x), "f"(x.y));
 }
 
 __device__ __forceinline__ void split2_pair(float2 x, uint32_t &h, uint32_t &l)
