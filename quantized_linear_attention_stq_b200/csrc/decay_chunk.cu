@@ -18,7 +18,8 @@
 //
 // Roles: warps 0-7 turn scores into P, add b O and P V and write o (two warps to each 32 rows, on
 // alternate groups of 16 columns of P and halves of O's columns); warps 8-15 keep S and write its terms;
-// warps 16-19 make e K, 16 tokens at a time; warp 20 issues the TMA loads, warp 21 the MMAs, warp 22
+// warps 16-19 make e K, 16 tokens at a time, warps 8-15 every other 16 of them (for sums only, warps 0-7 two
+// of three); warp 20 issues the TMA loads, warp 21 the MMAs, warp 22
 // makes the products of the decays. Products are issued as scores, O, dS, P V: P is made while O and dS
 // run, S's terms for the next chunk while P V and the next scores do. Roles meet at mbarriers only, each
 // waited for with a limit; a barrier's next phase needs its waiter's progress, so no wait can miss its
@@ -76,7 +77,7 @@ struct ChunkCfg {
     static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
     static constexpr int SLOTS = SUMS ? 8 : 2;          // of e K
     static constexpr uint32_t KT = SUMS ? 0 : TM_KT;
-    static constexpr int MAKERS = SUMS ? 3 : 1;         // groups of four warps that make e K
+    static constexpr int MAKERS = 3;                    // groups of four warps that make e K
 };
 
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int x, int t, int tile, uint32_t bar)
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(NTC, 1)
             if (i >= KE && i < KE + 3) count = 4 * M::MAKERS;
             if (i == GF) count = 20;
             if (i == PF || i == OS || i == OFF || i == DSF || i == SF) count = 8;
-            if (i >= KTF && i < KTF + 8) count = 4;
+            if (i >= KTF && i < KTF + 8) count = !SUMS && i == KTF + 1 ? 8 : 4;
             mbar_init(bar(i), count);
         }
         fence_mbar_init();
@@ -262,19 +263,22 @@ __global__ void __launch_bounds__(NTC, 1)
     // Terms of e K, tokens 16 j .. 16 j + 15 of chunk n: a row of Tensor Memory per entry of k, two tokens
     // to a column, which is how transposed 8 x 8 matrices lie in a warp's registers. Rows of v behind the
     // prompt's end hold other tokens and are zeroed here, before the MMAs of these tokens.
-    auto make_ek = [&](int n, int j) {
+    // The terms are made before the slot is waited for: a slot's way back and forth bounds dS.
+    // Parts x0 .. x1 - 1 of a warp's 32 entries, 16 each. A slot is always filled by the same warps: who waits
+    // for a slot has then seen the one before.
+    auto make_ek = [&](int n, int j, int x0, int x1) {
         const int slot_ = j % M::SLOTS, use = (8 * n + j) / M::SLOTS;
-        if (use > 0 && !wait(KTE + slot_, use - 1)) return;
-        umma::fence_after_sync();
         const int left = len - (n0 + n) * CT - 16 * j;  // tokens of the group that the prompt has
+        uint32_t hh[2][4], mm[2][4], ll[2][4];
         if (quarter < 2 * KB) {
             const float2 e[2] = {*reinterpret_cast<const float2 *>(&g.e[16 * j + 2 * (lane & 3)]),
                                  *reinterpret_cast<const float2 *>(&g.e[16 * j + 8 + 2 * (lane & 3)])};
             const int tok = 16 * j + (lane & 7) + (lane >> 4) * 8, c8 = 4 * (quarter & 1) + (lane >> 3 & 1);
             const uint32_t k = sb + M::K + (n % KS) * M::QB + (quarter >> 1) * BOX;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {  // 16 entries of k
-                uint32_t r[4], hh[4], mm[4], ll[4];
+            for (int x = 0; x < 2; ++x) {
+                if (x < x0 || x >= x1) continue;
+                uint32_t r[4];
                 ldmatrix4_trans(k + umma::sw128_chunk(tok, c8 + 2 * x), r);
                 if (left < 16)
 #pragma unroll
@@ -286,11 +290,19 @@ __global__ void __launch_bounds__(NTC, 1)
                 for (int i = 0; i < 4; ++i)
                     pf::split3_pair(__fmul2_rn(make_float2(__uint_as_float(r[i] << 16), __uint_as_float(r[i] & 0xFFFF0000u)),
                                                e[i >> 1]),
-                                    hh[i], mm[i], ll[i]);
+                                    hh[x][i], mm[x][i], ll[x][i]);
+            }
+        }
+        if (use > 0 && !wait(KTE + slot_, use - 1)) return;
+        umma::fence_after_sync();
+        if (quarter < 2 * KB) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (x < x0 || x >= x1) continue;
                 const uint32_t to = tl + ((uint32_t)(16 * x) << 16) + M::KT + slot_ * KT_COLS;
-                tmem_st_16x8(to, hh);
-                tmem_st_16x8(to + 8, mm);
-                tmem_st_16x8(to + 16, ll);
+                tmem_st_16x8(to, hh[x]);
+                tmem_st_16x8(to + 8, mm[x]);
+                tmem_st_16x8(to + 16, ll[x]);
             }
             tmem_wait_st();
         }
@@ -306,22 +318,21 @@ __global__ void __launch_bounds__(NTC, 1)
         umma::fence_before_sync();
         arrive(KTF + slot_);
     };
-    // ... of every chunk, by group `who` of the makers
-    auto make_all = [&](int who) {
-        for (int n = 0; n < N; ++n) {
-            if (!wait(GA, n) || !wait(FK + n % KS, n / KS)) break;
-            for (int j = who; j < 8 && ok; j += M::MAKERS) make_ek(n, j);
-            if (!ok) break;
-            arrive(KE + n % KS);
-            arrive(GF);
-        }
+    // ... of groups j = first, first + step, ... of a chunk
+    auto make_chunk = [&](int n, int first, int step, int x0, int x1) {
+        if (!wait(GA, n) || !wait(FK + n % KS, n / KS)) return;
+        for (int j = first; j < 8 && ok; j += step) make_ek(n, j, x0, x1);
+        if (ok) arrive(KE + n % KS);
     };
 
     if (warp < 8) {
         regs_up<96>();
         // ---- P, o -----------------------------------------------------------------------------
         if constexpr (SUMS) {
-            make_all(warp >> 2);
+            for (int n = 0; n < N && ok; ++n) {
+                make_chunk(n, warp >> 2, 3, 0, 2);
+                arrive(GF);
+            }
         } else {
             const int t = 32 * quarter + lane, sub = warp >> 2, l16 = lane & 15, top = 2 * quarter + 1;
             const bool hi = lane >= 16;
@@ -397,34 +408,34 @@ __global__ void __launch_bounds__(NTC, 1)
 
                 if (!wait(OF, n)) break;
                 umma::fence_after_sync();
+#pragma unroll
+                for (int cc = 0; cc < 32 * KB; cc += 16) {
+                    float x[16];
+                    pf::tmem_ld16(tl + TM_O + c0 + cc, x);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o1[cc + i] = fmaf(bt, o1[cc + i], x[i]);
+                }
+                umma::fence_before_sync();
+                arrive(OFF);
                 const bool whole = t0 + 32 * quarter + 32 <= len;  // every row of the warp is the prompt's
 #pragma unroll
                 for (int cc = 0; cc < 32 * KB; cc += 16) {
                     const int to = c0 + cc;
-                    float x[16];
-                    pf::tmem_ld16(tl + TM_O + to, x);
-                    if (cc + 16 == 32 * KB) {
-                        umma::fence_before_sync();
-                        arrive(OFF);
-                    }
+                    if (to >= d) break;
                     if ((cc & 31) == 0) {  // the tile's last use is over
                         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                         __syncwarp();
                     }
-                    if (to >= d) continue;
-                    float2 y[8];
+                    if (t0 + t < len)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        y[i] = __ffma2_rn(make_float2(bt, bt), make_float2(o1[cc + 2 * i], o1[cc + 2 * i + 1]),
-                                          make_float2(x[2 * i], x[2 * i + 1]));
-                        if (t0 + t < len) bad = __ffma2_rn(y[i], make_float2(0.f, 0.f), bad);
-                    }
+                        for (int i = 0; i < 16; i += 2)
+                            bad = __ffma2_rn(make_float2(o1[cc + i], o1[cc + i + 1]), make_float2(0.f, 0.f), bad);
                     if (whole) {
                         uint8_t *tile_o = sm + M::O + warp * 4096;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            *reinterpret_cast<float4 *>(tile_o + umma::sw128_chunk(lane, (cc & 31) / 4 + i)) =
-                                make_float4(y[2 * i].x, y[2 * i].y, y[2 * i + 1].x, y[2 * i + 1].y);
+                        for (int i = 0; i < 16; i += 4)
+                            *reinterpret_cast<float4 *>(tile_o + umma::sw128_chunk(lane, ((cc & 31) + i) / 4)) =
+                                make_float4(o1[cc + i], o1[cc + i + 1], o1[cc + i + 2], o1[cc + i + 3]);
                         if ((cc & 31) == 16 || to + 16 == d) {
                             umma::fence_proxy_async();
                             __syncwarp();
@@ -433,8 +444,8 @@ __global__ void __launch_bounds__(NTC, 1)
                     } else if (t0 + t < len) {
                         float *dst = p.o + (tile * p.T + t0 + t) * d + to;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            *reinterpret_cast<float4 *>(dst + 4 * i) = make_float4(y[2 * i].x, y[2 * i].y, y[2 * i + 1].x, y[2 * i + 1].y);
+                        for (int i = 0; i < 16; i += 4)
+                            *reinterpret_cast<float4 *>(dst + i) = make_float4(o1[cc + i], o1[cc + i + 1], o1[cc + i + 2], o1[cc + i + 3]);
                     }
                 }
             }
@@ -481,6 +492,7 @@ __global__ void __launch_bounds__(NTC, 1)
             if (!wait(GA, n)) break;
             const float bc = (float)g.all;
             upto *= g.all;
+            if (!SUMS) make_chunk(n, 1, 2, warp >> 2 & 1, (warp >> 2 & 1) + 1);
             arrive(GF);
             if (!wait(DS, n)) break;
             umma::fence_after_sync();
@@ -511,7 +523,10 @@ __global__ void __launch_bounds__(NTC, 1)
     } else if (warp < 20) {
         regs_down<40>();
         // ---- e K ----------------------------------------------------------------------------
-        make_all(M::MAKERS - 1);
+        for (int n = 0; n < N && ok; ++n) {
+            make_chunk(n, SUMS ? 2 : 0, SUMS ? 3 : 2, 0, 2);
+            arrive(GF);
+        }
     } else if (regs_down<40>(); warp == 20) {
         // ---- TMA ----------------------------------------------------------------------------
         if (elect_one()) {
