@@ -18,12 +18,13 @@
 //
 // Roles: warps 0-7 turn scores into P, add b O and P V and write o (two warps to each 32 rows, on
 // alternate groups of 16 columns of P and halves of O's columns); warps 8-15 keep S and write its terms;
-// warps 16-19 make e K, 16 tokens at a time, warps 8-15 every other 16 of them (for sums only, warps 0-7 two
-// of three); warp 20 issues the TMA loads, warp 21 the MMAs, warp 22
-// makes the products of the decays. Products are issued as scores, O, dS, P V: P is made while O and dS
-// run, S's terms for the next chunk while P V and the next scores do. Roles meet at mbarriers only, each
-// waited for with a limit; a barrier's next phase needs its waiter's progress, so no wait can miss its
-// phase.
+// warps 16-23 and 8-15 make e K, 16 tokens at a time, the ones of even and the others of odd groups (for
+// sums only, warps 0-7 instead of 8-15); warp 24 issues the TMA loads, warp 25 the MMAs, warp 26
+// makes the products of the decays. Products are issued as scores, dS, O, P V: P is made while dS and O
+// run, dS is read while O does (P V then takes its columns of Tensor Memory), S's terms for the next
+// chunk are made from the end of O on, o is read while the next scores run. Roles meet at mbarriers only,
+// each waited for with a limit; a barrier's next phase needs its waiter's progress, so no wait can miss
+// its phase.
 //
 // A group of 16 scores (16 fp32 columns of Tensor Memory) is replaced in place by the h and m terms of
 // its 16 entries of P (8 columns each); the l terms have columns of their own.
@@ -36,9 +37,9 @@ namespace stq {
 namespace {
 
 constexpr int CT = kDecayChunk;         // tokens of a chunk
-constexpr int NTC = 768;                // threads
+constexpr int NTC = 896;                // threads
 constexpr uint32_t BOX = CT * 128;      // a [128 tokens][64 columns] bf16 box
-// Tensor Memory columns: scores, then P's h and m terms; its l terms; O, then P V; dS; slots of e K's terms
+// Tensor Memory columns: scores, then P's h and m terms; its l terms; O; dS, then P V; slots of e K's terms
 constexpr uint32_t TM_SC = 0, TM_L = 128, TM_O = 192, TM_DS = 320, TM_KT = 448, KT_COLS = 24;
 
 // Decay products of a chunk, and inside groups of 16 tokens.
@@ -50,9 +51,8 @@ struct ChunkGates {
     double all;
 };
 
-// Loads of q, k, v landed; k free; v free (sums only); gates made / free; scores done; P made; O done /
-// read; P V done / read; e K's slots full / free; dS done / read; S's terms made; end.
-enum { FQ, FK, FV = FK + 3, KE = FV + 3, VE = KE + 3, GA = VE + 3, GF, SC, PF, QS, OS, OF, OFF, KTF, KTE = KTF + 8, DS = KTE + 8, DSF, SF, END, NBAR };
+// Loads of q, k, v landed; k free; v free; gates made / free; scores done; P made; O done; P V done; o read; e K's slots full / free; dS done / read; S's terms made; end.
+enum { FQ, FK, FV = FK + 3, KE = FV + 3, VE = KE + 3, GA = VE + 3, GF, SC, PF, QS, OF, OFF, KTF, KTE = KTF + 8, DS = KTE + 8, DSF, SF, END, NBAR };
 
 struct ChunkMisc {
     unsigned long long bars[NBAR];
@@ -64,20 +64,21 @@ template <int KB, int SUMS>
 struct ChunkCfg {
     static constexpr uint32_t QB = KB * BOX;            // bytes of a q, k or v tile
     static constexpr int KS = SUMS ? 3 : 1;             // stages of k
-    static constexpr int VS = SUMS ? 3 : 1;             // stages of v
+    static constexpr int VS = SUMS ? 3 : 2;             // stages of v
     static constexpr uint32_t K = 0;
     static constexpr uint32_t V = K + KS * QB;
     static constexpr uint32_t Q = V + VS * QB;
     static constexpr uint32_t ST = Q + (SUMS ? 0 : QB); // three terms of S: [KB][64 KB rows][64 columns]
     static constexpr uint32_t SA = KB * 64 * 128;       // ... bytes of 64 columns
     static constexpr uint32_t STB = KB * SA;            // ... of a term
-    static constexpr uint32_t O = ST + (SUMS ? 0 : 3 * STB);  // [32 rows][32 columns] of o for each of 8 warps
-    static constexpr uint32_t MISC = O + (SUMS ? 0 : 8 * 4096);
+    // [32 rows][32 columns] of o for each of 8 warps: the chunk's v for d = 128, where P V is done with it
+    static constexpr uint32_t O = KB == 2 ? V : ST + (SUMS ? 0 : 3 * STB);
+    static constexpr uint32_t OB = KB == 2 ? QB : 0;    // ... from one stage to the next
+    static constexpr uint32_t MISC = ST + (SUMS ? 0 : 3 * STB) + (SUMS || KB == 2 ? 0 : 8 * 4096);
     static constexpr uint32_t SMEM = MISC + sizeof(ChunkMisc);
     static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
     static constexpr int SLOTS = SUMS ? 8 : 2;          // of e K
     static constexpr uint32_t KT = SUMS ? 0 : TM_KT;
-    static constexpr int MAKERS = 3;                    // groups of four warps that make e K
 };
 
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int x, int t, int tile, uint32_t bar)
@@ -126,6 +127,23 @@ __device__ __forceinline__ void tmem_st_16x8(uint32_t taddr, const uint32_t (&r)
                  : "memory");
 }
 
+// The same sixteen columns as pf::tmem_ld16, not there before tmem_wait_ld16.
+__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+
 // Four transposed 8 x 8 matrices of 16-bit entries from shared memory.
 __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4])
 {
@@ -139,13 +157,6 @@ __device__ __forceinline__ void tma_prefetch(const CUtensorMap *map, int x, int 
 {
     asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(t), "r"(tile)
                  : "memory");
-}
-__device__ __forceinline__ void tma_store(const CUtensorMap *map, uint32_t src, int x, int t, int tile)
-{
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x), "r"(t),
-                 "r"(tile), "r"(src)
-                 : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
 // D[tmem] (+)= A[smem] * B[smem], one of several products of the same A in a row: the first (0) leaves A in
@@ -174,7 +185,7 @@ __device__ __forceinline__ void mma_same_a(uint32_t d, uint64_t a, uint64_t b, u
 }
 
 // A thread's registers beyond or below those of the launch, by whole groups of four warps: 256 threads at
-// 96, 256 at 104 and 256 at 40 are the 768 at 80 that the launch has.
+// 96, 256 at 88, 256 at 32 and 128 at 72 are the 896 at 72 that the launch has.
 template <int N>
 __device__ __forceinline__ void regs_up()
 {
@@ -198,8 +209,7 @@ __device__ __forceinline__ bool elect_one()
 template <int KB, int SUMS>
 __global__ void __launch_bounds__(NTC, 1)
     decay_chunk_kernel(const __grid_constant__ DecayParams p, const int d, const __grid_constant__ CUtensorMap mq,
-                       const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-                       const __grid_constant__ CUtensorMap mo)
+                       const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv)
 {
     using M = ChunkCfg<KB, SUMS>;
     constexpr int KS = M::KS, VS = M::VS;
@@ -229,15 +239,16 @@ __global__ void __launch_bounds__(NTC, 1)
     if (tid == 0) {
         for (int i = 0; i < NBAR; ++i) {
             int count = 1;
-            if (i >= KE && i < KE + 3) count = 4 * M::MAKERS;
-            if (i == GF) count = 20;
-            if (i == PF || i == OS || i == OFF || i == DSF || i == SF) count = 8;
-            if (i >= KTF && i < KTF + 8) count = !SUMS && i == KTF + 1 ? 8 : 4;
+            if (i >= KE && i < KE + 3) count = 16;
+            if (i == GF) count = 24;
+            if (i >= VE && i < VE + 3) count = SUMS ? 1 : 8;
+            if (i == PF || i == OFF || i == DSF || i == SF) count = 8;
+            if (i >= KTF && i < KTF + 8) count = 8;
             mbar_init(bar(i), count);
         }
         fence_mbar_init();
     }
-    if (warp == 21) umma::tmem_alloc(smem_u32(&ms.tmem), 512);
+    if (warp == 25) umma::tmem_alloc(smem_u32(&ms.tmem), 512);
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
@@ -247,7 +258,11 @@ __global__ void __launch_bounds__(NTC, 1)
     const ChunkGates &g = ms.g;
     // a wait that gave up ends its role; the other roles' waits then give up too
     bool ok = true;
-    auto wait = [&](int i, int phase) { return ok = ok && pf::wait_bar(bar(i), (uint32_t)phase & 1u, p.status); };
+    auto wait = [&](int i, int phase) {  // of a warp
+        const uint32_t at = bar(i), parity = (uint32_t)phase & 1u;
+        if (!__all_sync(0xffffffffu, mbar_try_wait(at, parity))) ok = ok && pf::wait_bar(at, parity, p.status);
+        return ok;
+    };
     auto once = [&](int i, int phase) {  // of one thread
         if (ok && !mbar_wait_bounded(bar(i), (uint32_t)phase & 1u)) {
             ok = false;
@@ -263,47 +278,37 @@ __global__ void __launch_bounds__(NTC, 1)
     // Terms of e K, tokens 16 j .. 16 j + 15 of chunk n: a row of Tensor Memory per entry of k, two tokens
     // to a column, which is how transposed 8 x 8 matrices lie in a warp's registers. Rows of v behind the
     // prompt's end hold other tokens and are zeroed here, before the MMAs of these tokens.
-    // The terms are made before the slot is waited for: a slot's way back and forth bounds dS.
-    // Parts x0 .. x1 - 1 of a warp's 32 entries, 16 each. A slot is always filled by the same warps: who waits
-    // for a slot has then seen the one before.
-    auto make_ek = [&](int n, int j, int x0, int x1) {
+    // The terms are made before the slot is waited for: a slot's way back and forth bounds dS. A warp makes
+    // those of 16 of its quarter's 32 entries of k (x: which). A slot is always filled by the same warps: who
+    // waits for it to be free has then seen it free before.
+    auto make_ek = [&](int n, int j, int x) {
         const int slot_ = j % M::SLOTS, use = (8 * n + j) / M::SLOTS;
         const int left = len - (n0 + n) * CT - 16 * j;  // tokens of the group that the prompt has
-        uint32_t hh[2][4], mm[2][4], ll[2][4];
+        uint32_t hh[4], mm[4], ll[4];
         if (quarter < 2 * KB) {
-            const float2 e[2] = {*reinterpret_cast<const float2 *>(&g.e[16 * j + 2 * (lane & 3)]),
-                                 *reinterpret_cast<const float2 *>(&g.e[16 * j + 8 + 2 * (lane & 3)])};
-            const int tok = 16 * j + (lane & 7) + (lane >> 4) * 8, c8 = 4 * (quarter & 1) + (lane >> 3 & 1);
-            const uint32_t k = sb + M::K + (n % KS) * M::QB + (quarter >> 1) * BOX;
+            uint32_t r[4];
+            const int tok = 16 * j + (lane & 7) + (lane >> 4) * 8, c8 = 4 * (quarter & 1) + 2 * x + (lane >> 3 & 1);
+            ldmatrix4_trans(sb + M::K + (n % KS) * M::QB + (quarter >> 1) * BOX + umma::sw128_chunk(tok, c8), r);
+            if (left < 16)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                if (x < x0 || x >= x1) continue;
-                uint32_t r[4];
-                ldmatrix4_trans(k + umma::sw128_chunk(tok, c8 + 2 * x), r);
-                if (left < 16)
+                for (int i = 0; i < 4; ++i) {
+                    const int u = left - 8 * (i >> 1) - 2 * (lane & 3);
+                    r[i] = u >= 2 ? r[i] : u == 1 ? r[i] & 0xFFFFu : 0u;
+                }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int u = left - 8 * (i >> 1) - 2 * (lane & 3);
-                        r[i] = u >= 2 ? r[i] : u == 1 ? r[i] & 0xFFFFu : 0u;
-                    }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    pf::split3_pair(__fmul2_rn(make_float2(__uint_as_float(r[i] << 16), __uint_as_float(r[i] & 0xFFFF0000u)),
-                                               e[i >> 1]),
-                                    hh[x][i], mm[x][i], ll[x][i]);
+            for (int i = 0; i < 4; ++i) {
+                const float2 e = *reinterpret_cast<const float2 *>(&g.e[16 * j + 8 * (i >> 1) + 2 * (lane & 3)]);
+                pf::split3_pair(make_float2(__uint_as_float(r[i] << 16) * e.x, __uint_as_float(r[i] & 0xFFFF0000u) * e.y),
+                                hh[i], mm[i], ll[i]);
             }
         }
         if (use > 0 && !wait(KTE + slot_, use - 1)) return;
         umma::fence_after_sync();
         if (quarter < 2 * KB) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                if (x < x0 || x >= x1) continue;
-                const uint32_t to = tl + ((uint32_t)(16 * x) << 16) + M::KT + slot_ * KT_COLS;
-                tmem_st_16x8(to, hh[x]);
-                tmem_st_16x8(to + 8, mm[x]);
-                tmem_st_16x8(to + 16, ll[x]);
-            }
+            const uint32_t to = tl + ((uint32_t)(16 * x) << 16) + M::KT + slot_ * KT_COLS;
+            tmem_st_16x8(to, hh);
+            tmem_st_16x8(to + 8, mm);
+            tmem_st_16x8(to + 16, ll);
             tmem_wait_st();
         }
         if (left < 16) {
@@ -321,7 +326,10 @@ __global__ void __launch_bounds__(NTC, 1)
     // ... of groups j = first, first + step, ... of a chunk
     auto make_chunk = [&](int n, int first, int step, int x0, int x1) {
         if (!wait(GA, n) || !wait(FK + n % KS, n / KS)) return;
-        for (int j = first; j < 8 && ok; j += step) make_ek(n, j, x0, x1);
+#pragma unroll 1
+        for (int j = first; j < 8; j += step)
+#pragma unroll 1
+            for (int x = x0; x < x1 && ok; ++x) make_ek(n, j, x);
         if (ok) arrive(KE + n % KS);
     };
 
@@ -330,7 +338,7 @@ __global__ void __launch_bounds__(NTC, 1)
         // ---- P, o -----------------------------------------------------------------------------
         if constexpr (SUMS) {
             for (int n = 0; n < N && ok; ++n) {
-                make_chunk(n, warp >> 2, 3, 0, 2);
+                make_chunk(n, warp >> 2, 4, 0, 2);
                 arrive(GF);
             }
         } else {
@@ -339,7 +347,7 @@ __global__ void __launch_bounds__(NTC, 1)
             const uint32_t z[16] = {}, z8[8] = {};
             for (int c = top + 1 + sub; c < 8; c += 2)  // tokens behind the row's: zero in every chunk
                 tmem_st8(tl + TM_L + 8 * c, z8);
-            float2 bad = make_float2(0.f, 0.f);  // 0 x is not 0 for an x that is not finite
+            float bad[4] = {};  // 0 x is not 0 for an x that is not finite
             for (int n = 0; n < N; ++n) {
                 const int t0 = (n0 + n) * CT;
                 if (!wait(GA, n)) break;
@@ -350,16 +358,20 @@ __global__ void __launch_bounds__(NTC, 1)
                 // The topmost group: of the two halves of the rows one has its diagonal there. The other has
                 // nothing (sub 0), or all of the group below its own (sub 1).
                 int c = top - sub;
+                uint32_t next[16];  // scores, loaded a group ahead
                 {
-                    float v[16], D = 0.f, x[16];
-                    pf::tmem_ld16(tl + TM_SC + 16 * c, v);
+                    float D = 0.f, x[16];
+                    uint32_t v[16];
+                    tmem_ld16_async(tl + TM_SC + 16 * c, v);
+                    tmem_wait_ld16(v);
+                    if (c >= 2) tmem_ld16_async(tl + TM_SC + 16 * (c - 2), next);
                     const bool diag = hi == (sub == 0);
 #pragma unroll
                     for (int i = 15; i >= 0; --i) {
                         if (i < 15) D *= g.alpha[16 * c + i + 1];
                         if (i >= l16) D = 1.f;
                         const float w = diag ? D : g.behind[16 * c + i] * upto;
-                        x[i] = (diag ? i > l16 : sub == 0) ? 0.f : v[i] * w;
+                        x[i] = (diag ? i > l16 : sub == 0) ? 0.f : __uint_as_float(v[i]) * w;
                     }
                     uint32_t hm[16], ll[8];
 #pragma unroll
@@ -372,7 +384,10 @@ __global__ void __launch_bounds__(NTC, 1)
 #pragma unroll 1
                 for (c -= 2; c >= 0; c -= 2) {
                     float v[16];
-                    pf::tmem_ld16(tl + TM_SC + 16 * c, v);
+                    tmem_wait_ld16(next);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(next[i]);
+                    if (c >= 2) tmem_ld16_async(tl + TM_SC + 16 * (c - 2), next);
                     uint32_t hm[16], ll[8];
 #pragma unroll
                     for (int i = 0; i < 16; i += 4) {
@@ -392,68 +407,59 @@ __global__ void __launch_bounds__(NTC, 1)
                 arrive(PF);
                 arrive(GF);
 
-                if (!wait(QS, n)) break;
-                umma::fence_after_sync();
-                const int c0 = 32 * KB * sub;
-                float o1[32 * KB];
-#pragma unroll
-                for (int cc = 0; cc < 32 * KB; cc += 16) {
-                    float x[16];
-                    pf::tmem_ld16(tl + TM_O + c0 + cc, x);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o1[cc + i] = x[i];
-                }
-                umma::fence_before_sync();
-                arrive(OS);
-
                 if (!wait(OF, n)) break;
                 umma::fence_after_sync();
+                const int c0 = 32 * KB * sub;
+                // through shared memory, so that a store covers whole lines: four rows of 32 columns
+                uint8_t *tile_o = sm + M::O + (n & 1) * M::OB + warp * 4096;
+                const int row = lane >> 3, left = 4 * (lane & 7) < d ? len - t0 - 32 * quarter - row : 0;
+                float *dst = p.o + (tile * p.T + t0 + 32 * quarter + row) * d + c0 + 4 * (lane & 7);
+                float o[KB][32];
 #pragma unroll
-                for (int cc = 0; cc < 32 * KB; cc += 16) {
-                    float x[16];
-                    pf::tmem_ld16(tl + TM_O + c0 + cc, x);
+                for (int cc = 0; cc < KB; ++cc) {
+                    umma::tmem_ld32(tl + TM_O + c0 + 32 * cc, o[cc]);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o1[cc + i] = fmaf(bt, o1[cc + i], x[i]);
+                    for (int i = 0; i < 32; i += 16) {
+                        float x[16];
+                        pf::tmem_ld16(tl + TM_DS + c0 + 32 * cc + i, x);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[cc][i + e] = fmaf(bt, o[cc][i + e], x[e]);
+                    }
                 }
                 umma::fence_before_sync();
                 arrive(OFF);
-                const bool whole = t0 + 32 * quarter + 32 <= len;  // every row of the warp is the prompt's
 #pragma unroll
-                for (int cc = 0; cc < 32 * KB; cc += 16) {
-                    const int to = c0 + cc;
-                    if (to >= d) break;
-                    if ((cc & 31) == 0) {  // the tile's last use is over
-                        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                        __syncwarp();
-                    }
+                for (int cc = 0; cc < KB; ++cc) {
+                    if (c0 + 32 * cc >= d) break;
                     if (t0 + t < len)
 #pragma unroll
-                        for (int i = 0; i < 16; i += 2)
-                            bad = __ffma2_rn(make_float2(o1[cc + i], o1[cc + i + 1]), make_float2(0.f, 0.f), bad);
-                    if (whole) {
-                        uint8_t *tile_o = sm + M::O + warp * 4096;
+                        for (int i = 0; i < 32; ++i)
+                            if (i < 16 || d > 16) bad[i & 3] = fmaf(o[cc][i], 0.f, bad[i & 3]);
 #pragma unroll
-                        for (int i = 0; i < 16; i += 4)
-                            *reinterpret_cast<float4 *>(tile_o + umma::sw128_chunk(lane, ((cc & 31) + i) / 4)) =
-                                make_float4(o1[cc + i], o1[cc + i + 1], o1[cc + i + 2], o1[cc + i + 3]);
-                        if ((cc & 31) == 16 || to + 16 == d) {
-                            umma::fence_proxy_async();
-                            __syncwarp();
-                            if (lane == 0) tma_store(&mo, sb + M::O + warp * 4096, to & ~31, t0 + 32 * quarter, (int)tile);
-                        }
-                    } else if (t0 + t < len) {
-                        float *dst = p.o + (tile * p.T + t0 + t) * d + to;
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<float4 *>(tile_o + umma::sw128_chunk(lane, i / 4)) =
+                            make_float4(o[cc][i], o[cc][i + 1], o[cc][i + 2], o[cc][i + 3]);
+                    __syncwarp();
+                    float *to = dst + 32 * cc;
+#pragma unroll 1
+                    for (int i = 0; i < 8; i += 4) {
+                        float4 x[4];
 #pragma unroll
-                        for (int i = 0; i < 16; i += 4)
-                            *reinterpret_cast<float4 *>(dst + i) = make_float4(o1[cc + i], o1[cc + i + 1], o1[cc + i + 2], o1[cc + i + 3]);
+                        for (int e = 0; e < 4; ++e)
+                            x[e] = *reinterpret_cast<const float4 *>(tile_o + umma::sw128_chunk(row + 4 * (i + e), lane & 7));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e, to += 4 * d)
+                            if (4 * (i + e) < left) __stcs(reinterpret_cast<float4 *>(to), x[e]);
                     }
+                    __syncwarp();
                 }
+                umma::fence_proxy_async();  // the tile's next writer is a copy
+                arrive(VE + n % VS);
             }
-            if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-            if (!(bad.x + bad.y == 0.f)) flag(p.status, kFlagNonfinite);
+            if (!(bad[0] + bad[1] + bad[2] + bad[3] == 0.f)) flag(p.status, kFlagNonfinite);
         }
     } else if (warp < 16) {
-        regs_up<104>();
+        regs_up<88>();
         // ---- S ----------------------------------------------------------------------------------
         constexpr int SC_ = 32 * KB;  // columns of a thread
         const int i = 32 * quarter + lane, c0 = SC_ * (warp >> 2 & 1);
@@ -505,7 +511,10 @@ __global__ void __launch_bounds__(NTC, 1)
             }
             umma::fence_before_sync();
             arrive(DSF);
-            if (!SUMS && n + 1 < N) put_state();  // O of this chunk was done before dS
+            if (!SUMS && n + 1 < N) {
+                if (!wait(QS, n)) break;
+                put_state();
+            }
         }
         if (ok && (SUMS || last)) {
             float *to = SUMS ? record : pool;
@@ -520,14 +529,15 @@ __global__ void __launch_bounds__(NTC, 1)
             if (bad) flag(p.status, kFlagNonfinite);
             if (SUMS && tid == 256) p.products[tile * p.segments + seg] = (float)upto;
         }
-    } else if (warp < 20) {
-        regs_down<40>();
+    } else if (warp < 24) {
+        regs_down<32>();
         // ---- e K ----------------------------------------------------------------------------
         for (int n = 0; n < N && ok; ++n) {
-            make_chunk(n, SUMS ? 2 : 0, SUMS ? 3 : 2, 0, 2);
+            const int x = warp >> 2 & 1;
+            SUMS ? make_chunk(n, 2 + x, 4, 0, 2) : make_chunk(n, 0, 2, x, x + 1);
             arrive(GF);
         }
-    } else if (regs_down<40>(); warp == 20) {
+    } else if (warp == 24) {
         // ---- TMA ----------------------------------------------------------------------------
         if (elect_one()) {
             auto load = [&](uint32_t to, const CUtensorMap *map, int n, int full) {
@@ -537,36 +547,30 @@ __global__ void __launch_bounds__(NTC, 1)
             };
             int nq = 0, nk = 0, nv = 0;  // loads issued
             for (int n = 0; n < N; ++n) {
-                if (n + 1 < N)  // the next chunk to L2: the loads below start late
-                    for (int x = 0; x < KB; ++x) {
-                        const int t = (n0 + n + 1) * CT;
-                        tma_prefetch(&mk, 64 * x, t, (int)tile);
-                        if (!SUMS) tma_prefetch(&mq, 64 * x, t, (int)tile);
-                        tma_prefetch(&mv, 64 * x, t, (int)tile);
-                    }
-                if constexpr (SUMS) {
-                    if (n >= KS && !once(KE + n % KS, n / KS - 1)) break;
-                    load(M::K + n % KS * M::QB, &mk, n, FK + n % KS);
-                    ++nk;
-                    if (n >= VS && !once(VE + n % VS, n / VS - 1)) break;
-                } else {
-                    if (n >= 1 && !once(QS, n - 1)) break;  // the scores were done before O
-                    load(M::Q, &mq, n, FQ);
-                    ++nq;
-                    if (n >= 1 && !once(KE, n - 1)) break;
-                    load(M::K, &mk, n, FK);
-                    ++nk;
-                    if (n >= 1 && !once(OF, n - 1)) break;
-                }
+                if (n >= VS && !once(VE + n % VS, n / VS - 1)) break;
                 load(M::V + n % VS * M::QB, &mv, n, FV + n % VS);
                 ++nv;
+                if (n >= KS && !once(KE + n % KS, n / KS - 1)) break;
+                if (!SUMS && n >= 1 && !once(SC, n - 1)) break;
+                load(M::K + n % KS * M::QB, &mk, n, FK + n % KS);
+                ++nk;
+                if constexpr (!SUMS) {
+                    if (n + 1 < N)  // the next chunk to L2: these loads start late
+                        for (int x = 0; x < KB; ++x) {
+                            tma_prefetch(&mk, 64 * x, (n0 + n + 1) * CT, (int)tile);
+                            tma_prefetch(&mq, 64 * x, (n0 + n + 1) * CT, (int)tile);
+                        }
+                    if (n >= 1 && !once(QS, n - 1)) break;  // the scores were done before
+                    load(M::Q, &mq, n, FQ);
+                    ++nq;
+                }
             }
             // no copy is in flight when the CTA ends, also where a wait gave up
             if (nq) mbar_wait_bounded(bar(FQ), (uint32_t)(nq - 1) & 1u);
             for (int n = nk - KS < 0 ? 0 : nk - KS; n < nk; ++n) mbar_wait_bounded(bar(FK + n % KS), (uint32_t)(n / KS) & 1u);
             for (int n = nv - VS < 0 ? 0 : nv - VS; n < nv; ++n) mbar_wait_bounded(bar(FV + n % VS), (uint32_t)(n / VS) & 1u);
         }
-    } else if (warp == 21) {
+    } else if (warp == 25) {
         // ---- MMA ----------------------------------------------------------------------------
         if (elect_one()) {
             const uint32_t cols = KB == 2 ? 128 : d;  // of v
@@ -588,19 +592,8 @@ __global__ void __launch_bounds__(NTC, 1)
                             umma::mma_bf16(tmem + TM_SC, dq + (((kk >> 2) * BOX + (kk & 3) * 32) >> 4),
                                            kn + (((kk >> 2) * BOX + (kk & 3) * 32) >> 4), id_sc, kk != 0);
                     umma::mma_commit(bar(SC));
-                    if (!once(SF, n) || (n > 0 && !once(OFF, n - 1))) break;
-                    umma::fence_after_sync();
-#pragma unroll
-                    for (int kk = 0; kk < 4 * KB; ++kk)
-                        if (kk < steps) {
-                            const uint64_t a = dq + (((kk >> 2) * BOX + (kk & 3) * 32) >> 4), s = ds + (kk * 2048 >> 4);
-                            mma_same_a<0>(tmem + TM_O, a, s + (2 * M::STB >> 4), id_d, kk != 0);
-                            mma_same_a<1>(tmem + TM_O, a, s + (M::STB >> 4), id_d, 1);
-                            mma_same_a<2>(tmem + TM_O, a, s, id_d, 1);
-                        }
-                    umma::mma_commit(bar(QS));
                 }
-                if (!once(FV + n % VS, n / VS) || (n > 0 && !once(DSF, n - 1))) break;
+                if (!once(FV + n % VS, n / VS) || (n > 0 && !once(SUMS ? DSF : OFF, n - 1))) break;
                 // rows d.. of dS are not read
 #pragma unroll 1
                 for (int j = 0; j < 8; ++j) {
@@ -619,13 +612,25 @@ __global__ void __launch_bounds__(NTC, 1)
                 if constexpr (SUMS) {
                     umma::mma_commit(bar(VE + n % VS));
                 } else {
-                    if (!once(PF, n) || !once(OS, n)) break;
+                    // (steps of O between the groups of dS shorten a chunk by a tenth in cycles, but at the power
+                    // limit the whole took 800 us so, and takes 747 us in this order)
+                    if (!once(SF, n)) break;
+                    umma::fence_after_sync();
+#pragma unroll 1
+                    for (int kk = 0; kk < steps; ++kk) {
+                        const uint64_t a = dq + (((kk >> 2) * BOX + (kk & 3) * 32) >> 4), s = ds + (kk * 2048 >> 4);
+                        mma_same_a<0>(tmem + TM_O, a, s + (2 * M::STB >> 4), id_d, kk != 0);
+                        mma_same_a<1>(tmem + TM_O, a, s + (M::STB >> 4), id_d, 1);
+                        mma_same_a<2>(tmem + TM_O, a, s, id_d, 1);
+                    }
+                    umma::mma_commit(bar(QS));
+                    if (!once(PF, n) || !once(DSF, n)) break;
                     umma::fence_after_sync();
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) mma_ts(tmem + TM_O, tmem + TM_L + 8 * kk, vn + (kk * 2048 >> 4), id_d, kk != 0);
+                    for (int kk = 0; kk < 8; ++kk) mma_ts(tmem + TM_DS, tmem + TM_L + 8 * kk, vn + (kk * 2048 >> 4), id_d, kk != 0);
 #pragma unroll
                     for (int kk = 0; kk < 16; ++kk)
-                        mma_ts(tmem + TM_O, tmem + TM_SC + 16 * (kk & 7) + (kk < 8 ? 8 : 0), vn + ((kk & 7) * 2048 >> 4), id_d, 1);
+                        mma_ts(tmem + TM_DS, tmem + TM_SC + 16 * (kk & 7) + (kk < 8 ? 8 : 0), vn + ((kk & 7) * 2048 >> 4), id_d, 1);
                     umma::mma_commit(bar(OF));
                 }
             }
@@ -633,7 +638,7 @@ __global__ void __launch_bounds__(NTC, 1)
             umma::mma_commit(bar(END));
             mbar_wait_bounded(bar(END), 0);
         }
-    } else if (warp == 22) {
+    } else if (warp == 26) {
         // ---- products of the decays: four tokens to a lane, four lanes to a group ----------------
         const float *alpha = p.alpha + tile * p.T;
         float next[4];
@@ -694,7 +699,7 @@ __global__ void __launch_bounds__(NTC, 1)
     }
     __syncwarp();
     __syncthreads();
-    if (warp == 21) umma::tmem_dealloc(tmem, 512);
+    if (warp == 25) umma::tmem_dealloc(tmem, 512);
 }
 
 template <int KB, int SUMS>
@@ -702,28 +707,24 @@ cudaError_t launch(const DecayParams &p, int d, cudaStream_t s)
 {
     const EncodeTiled enc = encode_tiled();
     if (!enc) return cudaErrorNotSupported;
-    // q, k, v as boxes of 128 tokens x 64 columns, o as boxes of 32 x 32; what lies outside is read as zeros
-    // and not written
-    CUtensorMap map[4];
-    const void *at[4] = {p.q, p.k, p.v, p.o};
-    for (int i = 0; i < 4; ++i) {
-        const cuuint64_t size = i < 3 ? 2 : 4, row = (cuuint64_t)d * size;
-        const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)p.T, (cuuint64_t)p.B * p.H};
-        const cuuint64_t strides[2] = {row, row * p.T};
-        const cuuint32_t box[3] = {i < 3 ? 64u : 32u, i < 3 ? (cuuint32_t)CT : 32u, 1}, estr[3] = {1, 1, 1};
-        if (enc(&map[i], i < 3 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
-                const_cast<void *>(at[i]), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    // boxes of 128 tokens x 64 columns; what lies outside the tensor is read as zeros
+    CUtensorMap map[3];
+    const void *in[3] = {p.q, p.k, p.v};
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)p.T, (cuuint64_t)p.B * p.H};
+    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)d * 2 * p.T};
+    const cuuint32_t box[3] = {64, CT, 1}, estr[3] = {1, 1, 1};
+    for (int i = 0; i < 3; ++i)
+        if (enc(&map[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(in[i]), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorNotSupported;
-    }
     auto kernel = decay_chunk_kernel<KB, SUMS>;
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ChunkCfg<KB, SUMS>::SMEM);
     if (e != cudaSuccess) return e;
     const int64_t grid = (int64_t)p.B * p.H * p.segments;
     if (grid > 0x7fffffff) return cudaErrorNotSupported;
-    kernel<<<(unsigned)grid, NTC, ChunkCfg<KB, SUMS>::SMEM, s>>>(p, d, map[0], map[1], map[2], map[3]);
+    kernel<<<(unsigned)grid, NTC, ChunkCfg<KB, SUMS>::SMEM, s>>>(p, d, map[0], map[1], map[2]);
     return cudaGetLastError();
 }
 
