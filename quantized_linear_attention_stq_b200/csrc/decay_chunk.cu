@@ -185,7 +185,7 @@ __device__ __forceinline__ void mma_same_a(uint32_t d, uint64_t a, uint64_t b, u
 }
 
 // A thread's registers beyond or below those of the launch, by whole groups of four warps: 256 threads at
-// 96, 256 at 88, 256 at 32 and 128 at 72 are the 896 at 72 that the launch has.
+// 96, 256 at 88, 256 at 40 and 128 at 56 are the 896 at 72 that the launch has.
 template <int N>
 __device__ __forceinline__ void regs_up()
 {
@@ -239,11 +239,11 @@ __global__ void __launch_bounds__(NTC, 1)
     if (tid == 0) {
         for (int i = 0; i < NBAR; ++i) {
             int count = 1;
-            if (i >= KE && i < KE + 3) count = 16;
+            if (i >= KE && i < KE + 3) count = SUMS ? 16 : 8;
             if (i == GF) count = 24;
             if (i >= VE && i < VE + 3) count = SUMS ? 1 : 8;
             if (i == PF || i == OFF || i == DSF || i == SF) count = 8;
-            if (i >= KTF && i < KTF + 8) count = 8;
+            if (i >= KTF && i < KTF + 8) count = 4;
             mbar_init(bar(i), count);
         }
         fence_mbar_init();
@@ -281,34 +281,42 @@ __global__ void __launch_bounds__(NTC, 1)
     // The terms are made before the slot is waited for: a slot's way back and forth bounds dS. A warp makes
     // those of 16 of its quarter's 32 entries of k (x: which). A slot is always filled by the same warps: who
     // waits for it to be free has then seen it free before.
-    auto make_ek = [&](int n, int j, int x) {
+    auto make_ek = [&](int n, int j) {
         const int slot_ = j % M::SLOTS, use = (8 * n + j) / M::SLOTS;
         const int left = len - (n0 + n) * CT - 16 * j;  // tokens of the group that the prompt has
-        uint32_t hh[4], mm[4], ll[4];
+        uint32_t hh[2][4], mm[2][4], ll[2][4];
         if (quarter < 2 * KB) {
-            uint32_t r[4];
-            const int tok = 16 * j + (lane & 7) + (lane >> 4) * 8, c8 = 4 * (quarter & 1) + 2 * x + (lane >> 3 & 1);
-            ldmatrix4_trans(sb + M::K + (n % KS) * M::QB + (quarter >> 1) * BOX + umma::sw128_chunk(tok, c8), r);
-            if (left < 16)
+            const int tok = 16 * j + (lane & 7) + (lane >> 4) * 8, c8 = 4 * (quarter & 1) + (lane >> 3 & 1);
+            const uint32_t k = sb + M::K + (n % KS) * M::QB + (quarter >> 1) * BOX;
+            const float2 e[2] = {*reinterpret_cast<const float2 *>(&g.e[16 * j + 2 * (lane & 3)]),
+                                 *reinterpret_cast<const float2 *>(&g.e[16 * j + 8 + 2 * (lane & 3)])};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int u = left - 8 * (i >> 1) - 2 * (lane & 3);
-                    r[i] = u >= 2 ? r[i] : u == 1 ? r[i] & 0xFFFFu : 0u;
-                }
+            for (int x = 0; x < 2; ++x) {
+                uint32_t r[4];
+                ldmatrix4_trans(k + umma::sw128_chunk(tok, c8 + 2 * x), r);
+                if (left < 16)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 e = *reinterpret_cast<const float2 *>(&g.e[16 * j + 8 * (i >> 1) + 2 * (lane & 3)]);
-                pf::split3_pair(make_float2(__uint_as_float(r[i] << 16) * e.x, __uint_as_float(r[i] & 0xFFFF0000u) * e.y),
-                                hh[i], mm[i], ll[i]);
+                    for (int i = 0; i < 4; ++i) {
+                        const int u = left - 8 * (i >> 1) - 2 * (lane & 3);
+                        r[i] = u >= 2 ? r[i] : u == 1 ? r[i] & 0xFFFFu : 0u;
+                    }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    pf::split3_pair(make_float2(__uint_as_float(r[i] << 16) * e[i >> 1].x,
+                                                __uint_as_float(r[i] & 0xFFFF0000u) * e[i >> 1].y),
+                                    hh[x][i], mm[x][i], ll[x][i]);
             }
         }
         if (use > 0 && !wait(KTE + slot_, use - 1)) return;
         umma::fence_after_sync();
         if (quarter < 2 * KB) {
-            const uint32_t to = tl + ((uint32_t)(16 * x) << 16) + M::KT + slot_ * KT_COLS;
-            tmem_st_16x8(to, hh);
-            tmem_st_16x8(to + 8, mm);
-            tmem_st_16x8(to + 16, ll);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const uint32_t to = tl + ((uint32_t)(16 * x) << 16) + M::KT + slot_ * KT_COLS;
+                tmem_st_16x8(to, hh[x]);
+                tmem_st_16x8(to + 8, mm[x]);
+                tmem_st_16x8(to + 16, ll[x]);
+            }
             tmem_wait_st();
         }
         if (left < 16) {
@@ -324,12 +332,10 @@ __global__ void __launch_bounds__(NTC, 1)
         arrive(KTF + slot_);
     };
     // ... of groups j = first, first + step, ... of a chunk
-    auto make_chunk = [&](int n, int first, int step, int x0, int x1) {
+    auto make_chunk = [&](int n, int first, int step) {
         if (!wait(GA, n) || !wait(FK + n % KS, n / KS)) return;
 #pragma unroll 1
-        for (int j = first; j < 8; j += step)
-#pragma unroll 1
-            for (int x = x0; x < x1 && ok; ++x) make_ek(n, j, x);
+        for (int j = first; j < 8 && ok; j += step) make_ek(n, j);
         if (ok) arrive(KE + n % KS);
     };
 
@@ -338,7 +344,7 @@ __global__ void __launch_bounds__(NTC, 1)
         // ---- P, o -----------------------------------------------------------------------------
         if constexpr (SUMS) {
             for (int n = 0; n < N && ok; ++n) {
-                make_chunk(n, warp >> 2, 4, 0, 2);
+                make_chunk(n, warp >> 2, 4);
                 arrive(GF);
             }
         } else {
@@ -498,7 +504,6 @@ __global__ void __launch_bounds__(NTC, 1)
             if (!wait(GA, n)) break;
             const float bc = (float)g.all;
             upto *= g.all;
-            if (!SUMS) make_chunk(n, 1, 2, warp >> 2 & 1, (warp >> 2 & 1) + 1);
             arrive(GF);
             if (!wait(DS, n)) break;
             umma::fence_after_sync();
@@ -530,14 +535,14 @@ __global__ void __launch_bounds__(NTC, 1)
             if (SUMS && tid == 256) p.products[tile * p.segments + seg] = (float)upto;
         }
     } else if (warp < 24) {
-        regs_down<32>();
+        regs_down<40>();
         // ---- e K ----------------------------------------------------------------------------
         for (int n = 0; n < N && ok; ++n) {
             const int x = warp >> 2 & 1;
-            SUMS ? make_chunk(n, 2 + x, 4, 0, 2) : make_chunk(n, 0, 2, x, x + 1);
+            SUMS ? make_chunk(n, 2 + x, 4) : make_chunk(n, x, 2);
             arrive(GF);
         }
-    } else if (warp == 24) {
+    } else if (regs_down<56>(); warp == 24) {
         // ---- TMA ----------------------------------------------------------------------------
         if (elect_one()) {
             auto load = [&](uint32_t to, const CUtensorMap *map, int n, int full) {
