@@ -599,6 +599,12 @@ __global__ void __launch_bounds__(NTC, 1)
                     umma::mma_commit(bar(SC));
                 }
                 if (!once(FV + n % VS, n / VS) || (n > 0 && !once(SUMS ? DSF : OFF, n - 1))) break;
+                auto o_step = [&](int kk) {
+                    const uint64_t a = dq + (((kk >> 2) * BOX + (kk & 3) * 32) >> 4), s = ds + (kk * 2048 >> 4);
+                    mma_same_a<0>(tmem + TM_O, a, s + (2 * M::STB >> 4), id_d, kk != 0);
+                    mma_same_a<1>(tmem + TM_O, a, s + (M::STB >> 4), id_d, 1);
+                    mma_same_a<2>(tmem + TM_O, a, s, id_d, 1);
+                };
                 // rows d.. of dS are not read
 #pragma unroll 1
                 for (int j = 0; j < 8; ++j) {
@@ -611,23 +617,21 @@ __global__ void __launch_bounds__(NTC, 1)
                     mma_ts(tmem + TM_DS, a + 8, v, id_d, 1);
                     mma_ts(tmem + TM_DS, a, v, id_d, 1);
                     umma::mma_commit(bar(KTE + slot_));
+                    // Steps of O between the groups of dS: a slot's way back and forth takes longer than the other
+                    // slot's products. The last steps are left for the time in which dS is read.
+                    if (!SUMS && j < 5 && j < steps) {
+                        if (j == 0 && !once(SF, n)) break;
+                        umma::fence_after_sync();
+                        o_step(j);
+                    }
                 }
                 if (!ok) break;
                 umma::mma_commit(bar(DS));
                 if constexpr (SUMS) {
                     umma::mma_commit(bar(VE + n % VS));
                 } else {
-                    // (steps of O between the groups of dS shorten a chunk by a tenth in cycles, but at the power
-                    // limit the whole took 800 us so, and takes 747 us in this order)
-                    if (!once(SF, n)) break;
-                    umma::fence_after_sync();
 #pragma unroll 1
-                    for (int kk = 0; kk < steps; ++kk) {
-                        const uint64_t a = dq + (((kk >> 2) * BOX + (kk & 3) * 32) >> 4), s = ds + (kk * 2048 >> 4);
-                        mma_same_a<0>(tmem + TM_O, a, s + (2 * M::STB >> 4), id_d, kk != 0);
-                        mma_same_a<1>(tmem + TM_O, a, s + (M::STB >> 4), id_d, 1);
-                        mma_same_a<2>(tmem + TM_O, a, s, id_d, 1);
-                    }
+                    for (int kk = 5; kk < steps; ++kk) o_step(kk);
                     umma::mma_commit(bar(QS));
                     if (!once(PF, n) || !once(DSF, n)) break;
                     umma::fence_after_sync();

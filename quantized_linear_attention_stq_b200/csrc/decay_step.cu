@@ -282,15 +282,17 @@ Split split(int B, int H, int T, int d, int in_bf16, bool cut)
     Split r{in_bf16 && T >= 64, 1, T};
     const int64_t tiles = (int64_t)B * H;
     if (r.chunk) {
-        // one CTA to an SM: rounds of CTAs times chunks of each, the first pass at 2/5 of the main
-        // one, the two launches more at three chunks
+        // One CTA to an SM: rounds of CTAs, each its chunks and 3.5 chunks' time of start and end (20 us; 5.5
+        // us a chunk). The first pass takes half of the main one's time, the join 1.5 chunks' and 0.15 a
+        // segment.
         const int64_t chunks = ((int64_t)T + kDecayChunk - 1) / kDecayChunk, ctas = tiles;
         double best = 0.0;
         int64_t per = chunks;
         for (int64_t n = 1; n <= (cut ? 64 : 1) && n <= chunks; ++n) {
             const int64_t c = (chunks + n - 1) / n;
             if ((chunks + c - 1) / c != n) continue;  // fewer segments of this length do
-            const double t = (double)((ctas * n + kSMs - 1) / kSMs) * c * (n > 1 ? 1.4 : 1.0) + (n > 1 ? 3.0 : 0.0);
+            double t = (double)((ctas * n + kSMs - 1) / kSMs) * ((double)c + 3.5);
+            if (n > 1) t += 0.5 * (double)((ctas * (n - 1) + kSMs - 1) / kSMs) * ((double)c + 3.5) + 1.5 + 0.15 * n;
             if (n == 1 || t < best) best = t, per = c;
         }
         r.segments = (int)((chunks + per - 1) / per);
