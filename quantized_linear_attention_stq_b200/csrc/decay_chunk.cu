@@ -127,6 +127,18 @@ __device__ __forceinline__ void tmem_st_16x8(uint32_t taddr, const uint32_t (&r)
                  : "memory");
 }
 
+// Eight columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8])
+{
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 // The same sixteen columns as pf::tmem_ld16, not there before tmem_wait_ld16.
 __device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16])
 {
@@ -302,8 +314,8 @@ __global__ void __launch_bounds__(NTC, 1)
                     }
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    pf::split3_pair(make_float2(__uint_as_float(r[i] << 16) * e[i >> 1].x,
-                                                __uint_as_float(r[i] & 0xFFFF0000u) * e[i >> 1].y),
+                    pf::split3_pair(__fmul2_rn(make_float2(__uint_as_float(r[i] << 16),
+                                                           __uint_as_float(r[i] & 0xFFFF0000u)), e[i >> 1]),
                                     hh[x][i], mm[x][i], ll[x][i]);
             }
         }
@@ -353,7 +365,7 @@ __global__ void __launch_bounds__(NTC, 1)
             const uint32_t z[16] = {}, z8[8] = {};
             for (int c = top + 1 + sub; c < 8; c += 2)  // tokens behind the row's: zero in every chunk
                 tmem_st8(tl + TM_L + 8 * c, z8);
-            float bad[4] = {};  // 0 x is not 0 for an x that is not finite
+            float bad = 0.f;  // 0 x is not 0 for an x that is not finite
             for (int n = 0; n < N; ++n) {
                 const int t0 = (n0 + n) * CT;
                 if (!wait(GA, n)) break;
@@ -416,31 +428,31 @@ __global__ void __launch_bounds__(NTC, 1)
                 if (!wait(OF, n)) break;
                 umma::fence_after_sync();
                 const int c0 = 32 * KB * sub;
-                // through shared memory, so that a store covers whole lines: four rows of 32 columns
-                uint8_t *tile_o = sm + M::O + (n & 1) * M::OB + warp * 4096;
-                const int row = lane >> 3, left = 4 * (lane & 7) < d ? len - t0 - 32 * quarter - row : 0;
-                float *dst = p.o + (tile * p.T + t0 + 32 * quarter + row) * d + c0 + 4 * (lane & 7);
                 float o[KB][32];
 #pragma unroll
                 for (int cc = 0; cc < KB; ++cc) {
                     umma::tmem_ld32(tl + TM_O + c0 + 32 * cc, o[cc]);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 16) {
-                        float x[16];
-                        pf::tmem_ld16(tl + TM_DS + c0 + 32 * cc + i, x);
+                    for (int i = 0; i < 32; i += 8) {  // (16 at a time spill where o has all its 64 columns)
+                        float x[8];
+                        tmem_ld8(tl + TM_DS + c0 + 32 * cc + i, x);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) o[cc][i + e] = fmaf(bt, o[cc][i + e], x[e]);
+                        for (int e = 0; e < 8; ++e) o[cc][i + e] = fmaf(bt, o[cc][i + e], x[e]);
                     }
                 }
                 umma::fence_before_sync();
                 arrive(OFF);
+                // through shared memory, so that a store covers whole lines: four rows of 32 columns
+                uint8_t *tile_o = sm + M::O + (n & 1) * M::OB + warp * 4096;
+                const int row = lane >> 3, left = 4 * (lane & 7) < d ? len - t0 - 32 * quarter - row : 0;
+                float *dst = p.o + (tile * p.T + t0 + 32 * quarter + row) * d + c0 + 4 * (lane & 7);
 #pragma unroll
                 for (int cc = 0; cc < KB; ++cc) {
                     if (c0 + 32 * cc >= d) break;
                     if (t0 + t < len)
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (i < 16 || d > 16) bad[i & 3] = fmaf(o[cc][i], 0.f, bad[i & 3]);
+                            if (i < 16 || d > 16) bad = fmaf(o[cc][i], 0.f, bad);
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)
                         *reinterpret_cast<float4 *>(tile_o + umma::sw128_chunk(lane, i / 4)) =
@@ -462,7 +474,7 @@ __global__ void __launch_bounds__(NTC, 1)
                 umma::fence_proxy_async();  // the tile's next writer is a copy
                 arrive(VE + n % VS);
             }
-            if (!(bad[0] + bad[1] + bad[2] + bad[3] == 0.f)) flag(p.status, kFlagNonfinite);
+            if (!(bad == 0.f)) flag(p.status, kFlagNonfinite);
         }
     } else if (warp < 16) {
         regs_up<88>();
