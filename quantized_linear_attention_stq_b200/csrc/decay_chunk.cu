@@ -171,6 +171,15 @@ __device__ __forceinline__ void tma_prefetch(const CUtensorMap *map, int x, int 
                  : "memory");
 }
 
+__device__ __forceinline__ void tma_store(const CUtensorMap *map, uint32_t src, int x, int t, int tile)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x), "r"(t),
+                 "r"(tile), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
 // D[tmem] (+)= A[smem] * B[smem], one of several products of the same A in a row: the first (0) leaves A in
 // the tensor core's buffer, the others take it from there, the last (2) lets it go.
 template <int TURN>
@@ -221,7 +230,8 @@ __device__ __forceinline__ bool elect_one()
 template <int KB, int SUMS>
 __global__ void __launch_bounds__(NTC, 1)
     decay_chunk_kernel(const __grid_constant__ DecayParams p, const int d, const __grid_constant__ CUtensorMap mq,
-                       const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv)
+                       const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                       const __grid_constant__ CUtensorMap mo)
 {
     using M = ChunkCfg<KB, SUMS>;
     constexpr int KS = M::KS, VS = M::VS;
@@ -424,6 +434,10 @@ __global__ void __launch_bounds__(NTC, 1)
                 umma::fence_before_sync();
                 arrive(PF);
                 arrive(GF);
+                if (n > 0) {  // the tile of the chunk before has left shared memory: v may be loaded there
+                    if (lane == 0) tma_stores_read();
+                    arrive(VE + (n - 1) % VS);
+                }
 
                 if (!wait(OF, n)) break;
                 umma::fence_after_sync();
@@ -442,38 +456,39 @@ __global__ void __launch_bounds__(NTC, 1)
                 }
                 umma::fence_before_sync();
                 arrive(OFF);
-                // through shared memory, so that a store covers whole lines: four rows of 32 columns
-                uint8_t *tile_o = sm + M::O + (n & 1) * M::OB + warp * 4096;
-                const int row = lane >> 3, left = 4 * (lane & 7) < d ? len - t0 - 32 * quarter - row : 0;
-                float *dst = p.o + (tile * p.T + t0 + 32 * quarter + row) * d + c0 + 4 * (lane & 7);
+                // through shared memory, by TMA, where the prompt has all of the warp's rows
+                const bool whole = t0 + 32 * quarter + 32 <= len;
+                const uint32_t tile_o = M::O + (n & 1) * M::OB + warp * 4096;
 #pragma unroll
                 for (int cc = 0; cc < KB; ++cc) {
-                    if (c0 + 32 * cc >= d) break;
+                    const int at = c0 + 32 * cc;
+                    if (at >= d) break;
                     if (t0 + t < len)
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (i < 16 || d > 16) bad = fmaf(o[cc][i], 0.f, bad);
+                    if (whole) {
+                        if (cc > 0) {
+                            if (lane == 0) tma_stores_read();
+                            __syncwarp();
+                        }
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        *reinterpret_cast<float4 *>(tile_o + umma::sw128_chunk(lane, i / 4)) =
-                            make_float4(o[cc][i], o[cc][i + 1], o[cc][i + 2], o[cc][i + 3]);
-                    __syncwarp();
-                    float *to = dst + 32 * cc;
-#pragma unroll 1
-                    for (int i = 0; i < 8; i += 4) {
-                        float4 x[4];
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<float4 *>(sm + tile_o + umma::sw128_chunk(lane, i / 4)) =
+                                make_float4(o[cc][i], o[cc][i + 1], o[cc][i + 2], o[cc][i + 3]);
+                        umma::fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0) tma_store(&mo, sb + tile_o, at, t0 + 32 * quarter, (int)tile);
+                    } else if (t0 + t < len) {
+                        float *dst = p.o + (tile * p.T + t0 + t) * d + at;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            x[e] = *reinterpret_cast<const float4 *>(tile_o + umma::sw128_chunk(row + 4 * (i + e), lane & 7));
-#pragma unroll
-                        for (int e = 0; e < 4; ++e, to += 4 * d)
-                            if (4 * (i + e) < left) __stcs(reinterpret_cast<float4 *>(to), x[e]);
+                        for (int i = 0; i < 32; i += 4)
+                            if (i < 16 || d > 16)
+                                *reinterpret_cast<float4 *>(dst + i) = make_float4(o[cc][i], o[cc][i + 1], o[cc][i + 2], o[cc][i + 3]);
                     }
-                    __syncwarp();
                 }
-                umma::fence_proxy_async();  // the tile's next writer is a copy
-                arrive(VE + n % VS);
             }
+            if (lane == 0) tma_stores_read();
             if (!(bad == 0.f)) flag(p.status, kFlagNonfinite);
         }
     } else if (warp < 16) {
@@ -728,24 +743,28 @@ cudaError_t launch(const DecayParams &p, int d, cudaStream_t s)
 {
     const EncodeTiled enc = encode_tiled();
     if (!enc) return cudaErrorNotSupported;
-    // boxes of 128 tokens x 64 columns; what lies outside the tensor is read as zeros
-    CUtensorMap map[3];
-    const void *in[3] = {p.q, p.k, p.v};
-    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)p.T, (cuuint64_t)p.B * p.H};
-    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)d * 2 * p.T};
-    const cuuint32_t box[3] = {64, CT, 1}, estr[3] = {1, 1, 1};
-    for (int i = 0; i < 3; ++i)
-        if (enc(&map[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(in[i]), dims, strides, box, estr,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    // q, k, v as boxes of 128 tokens x 64 columns, o of 32 x 32; what lies outside the tensor is read as zeros
+    // and not written
+    CUtensorMap map[4];
+    const void *at[4] = {p.q, p.k, p.v, p.o};
+    for (int i = 0; i < 4; ++i) {
+        const cuuint64_t row = (cuuint64_t)d * (i < 3 ? 2 : 4);
+        const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)p.T, (cuuint64_t)p.B * p.H};
+        const cuuint64_t strides[2] = {row, row * p.T};
+        const cuuint32_t box[3] = {i < 3 ? 64u : 32u, i < 3 ? (cuuint32_t)CT : 32u, 1}, estr[3] = {1, 1, 1};
+        if (enc(&map[i], i < 3 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
+                const_cast<void *>(at[i]), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorNotSupported;
+    }
     auto kernel = decay_chunk_kernel<KB, SUMS>;
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ChunkCfg<KB, SUMS>::SMEM);
     if (e != cudaSuccess) return e;
     const int64_t grid = (int64_t)p.B * p.H * p.segments;
     if (grid > 0x7fffffff) return cudaErrorNotSupported;
-    kernel<<<(unsigned)grid, NTC, ChunkCfg<KB, SUMS>::SMEM, s>>>(p, d, map[0], map[1], map[2]);
+    kernel<<<(unsigned)grid, NTC, ChunkCfg<KB, SUMS>::SMEM, s>>>(p, d, map[0], map[1], map[2], map[3]);
     return cudaGetLastError();
 }
 
