@@ -303,7 +303,7 @@ size_t stq_decay_prefill_workspace_bytes(int32_t B, int32_t H, int32_t T, int32_
 
 /* The same recurrence over prompts: token t of request b is the decay step on (q, k, v, alpha) at t.
  *   q, k, v     device [B][H][T][d] of in_dtype, 16-byte aligned
- *   alpha       device fp32 [B][H][T]
+ *   alpha       device fp32 [B][H][T]; products of up to 128 decays in a row have to stay finite
  *   lens        device int32 [B], tokens of each prompt, or NULL: T for all. Tokens behind a prompt's
  *               end change nothing: their rows of q, k, v and alpha are not used (NaN may stand
  *               there) and their rows of o stay as they were. A length outside [0, T] skips the
@@ -313,6 +313,8 @@ size_t stq_decay_prefill_workspace_bytes(int32_t B, int32_t H, int32_t T, int32_
  *               or NULL (slower where the size is not 0). A workspace that is given but too small or
  *               misaligned is STQ_ERR_INVALID_ARG; calls in flight at the same time need separate
  *               workspaces.
+ * Tokens are taken in chunks of 128 (bf16) and prompts in segments: an input that is not finite is
+ * flagged and may reach outputs of its head up to 127 tokens before it.
  * B == 0 or T == 0 is a no-op. */
 stq_status stq_decay_prefill(int32_t B, int32_t H, int32_t T, int32_t d, int32_t in_dtype, float *states,
                              int32_t state_slots, const int32_t *slots, const void *q, const void *k, const void *v,

@@ -8,9 +8,10 @@
 // its store, all loads of a thread in flight at once; a warp's lanes hold consecutive columns, so
 // rows move in whole 128-byte lines and the readout is a sum over the CTA's row groups.
 //
-// Token by token (fp32 inputs, short prompts). The state of a block of columns stays in registers for the whole prompt (columns
-// of S are independent of each other); tokens are staged through shared memory 32 at a time. A
-// column's rows are spread over SL lanes, joined by shuffles per token.
+// Token by token (fp32 inputs, short prompts). The state of a block of columns stays in registers for the
+// whole prompt (columns of S are independent of each other); tokens are staged through shared memory 16 or
+// 32 at a time. A column's rows are spread over SL lanes, joined by shuffles per token. Bound by the FMAs,
+// three to an entry and token (32 heads of 2048 tokens of d = 128: 284 us, of which 89 at the FMAs' rate).
 //
 // Segments. Where there are too few heads to fill the GPU, prompts are cut into segments: a first
 // pass over all but the last makes each segment's own sum (from an empty state) and the product of its
@@ -105,22 +106,23 @@ __global__ void __launch_bounds__(StepCfg<D>::NT) decay_step_kernel(const DecayP
     if (bad != 0.f) flag(p.status, kFlagNonfinite);  // x - x is 0 for a finite x, NaN otherwise
 }
 
-template <int D>
+template <int D, int CW>
 struct SerialCfg {
-    static constexpr int SL = D >= 32 ? 8 : 4;          // lanes sharing a column
-    static constexpr int RW = D / SL;                   // rows of a lane
-    static constexpr int CB = D < 32 ? D : 32;          // columns of a CTA
-    static constexpr int NT = CB * SL;
-    static constexpr int TB = 32;                       // tokens staged at a time
+    static constexpr int SL = D >= 32 ? 8 : 4;                     // lanes sharing a column
+    static constexpr int RW = D / SL;                              // rows of a thread
+    static constexpr int CB = CW == 1 ? (D < 32 ? D : 32) : (D < 64 ? D : 64);  // columns of a CTA
+    static constexpr int NT = CB / CW * SL;
+    static constexpr int TB = CW == 1 ? 32 : 16;                   // tokens staged at a time
 };
 
-template <int D, int IN_BF16, int SUMS>
-__global__ void __launch_bounds__(SerialCfg<D>::NT) decay_serial_kernel(const DecayParams p)
+template <int D, int IN_BF16, int SUMS, int CW>
+__global__ void __launch_bounds__(SerialCfg<D, CW>::NT) decay_serial_kernel(const DecayParams p)
 {
-    using S = SerialCfg<D>;
-    __shared__ __align__(16) float qs[S::TB][D], ks[S::TB][D];
-    __shared__ float vs[S::TB][S::CB], os[S::TB][S::CB], as[S::TB];
-    const int tid = threadIdx.x, r = tid % S::SL, cl = tid / S::SL;
+    using S = SerialCfg<D, CW>;
+    __shared__ __align__(16) float qs[SUMS ? 1 : S::TB][D], ks[S::TB][D];
+    __shared__ __align__(16) float vs[S::TB][S::CB], os[S::TB][S::CB];
+    __shared__ float as[S::TB];
+    const int tid = threadIdx.x, r = tid % S::SL, cl = tid / S::SL * CW;
     const int seg = blockIdx.x / (D / S::CB), c0 = blockIdx.x % (D / S::CB) * S::CB;
     const size_t tile = blockIdx.y + (size_t)blockIdx.z * gridDim.y;  // (request, head)
     if (tile >= (size_t)p.B * p.H) return;
@@ -138,55 +140,80 @@ __global__ void __launch_bounds__(SerialCfg<D>::NT) decay_serial_kernel(const De
     float *pool = p.states + ((size_t)slot * p.H + h) * (D * D) + c0 + cl;
     float *record = p.records ? p.records + (tile * p.segments + seg) * (D * D) + c0 + cl : nullptr;
     const float *before = p.segments > 1 ? record : pool;
-    // rows of a lane: groups of 4, SL groups apart, so that the lanes' 16-byte reads of k and q are adjacent
-    float s[S::RW];
+    // rows of a thread: groups of 4, SL groups apart, so that the lanes' 16-byte reads of k and q are adjacent
+    auto row = [&](int i) { return (size_t)((i / 4 * S::SL + r) * 4 + i % 4) * D; };
+    float s[S::RW][CW];
 #pragma unroll
-    for (int i = 0; i < S::RW; ++i) s[i] = SUMS ? 0.f : before[(size_t)((i / 4 * S::SL + r) * 4 + i % 4) * D];
+    for (int i = 0; i < S::RW; ++i)
+#pragma unroll
+        for (int c = 0; c < CW; ++c) s[i][c] = SUMS ? 0.f : before[row(i) + c];
     const size_t base = tile * (size_t)p.T;
     double upto = 1.0;
     for (int t0 = (int)from; t0 < end; t0 += S::TB) {
         const int n = end - t0 < S::TB ? end - t0 : S::TB;
-        for (int i = tid; i < n * D; i += S::NT) {
-            if (!SUMS) (&qs[0][0])[i] = load_in<IN_BF16>(p.q, (base + t0) * D + i);
-            (&ks[0][0])[i] = load_in<IN_BF16>(p.k, (base + t0) * D + i);
+        for (int i = 4 * tid; i < n * D; i += 4 * S::NT) {
+            if (!SUMS) *reinterpret_cast<float4 *>(&qs[0][0] + i) = load_in4<IN_BF16>(p.q, (base + t0) * D + i);
+            *reinterpret_cast<float4 *>(&ks[0][0] + i) = load_in4<IN_BF16>(p.k, (base + t0) * D + i);
         }
-        for (int i = tid; i < n * S::CB; i += S::NT)
-            vs[i / S::CB][i % S::CB] = load_in<IN_BF16>(p.v, (base + t0 + i / S::CB) * D + c0 + i % S::CB);
+        for (int i = 4 * tid; i < n * S::CB; i += 4 * S::NT)
+            *reinterpret_cast<float4 *>(&vs[0][0] + i) =
+                load_in4<IN_BF16>(p.v, (base + t0 + i / S::CB) * D + c0 + i % S::CB);
         for (int i = tid; i < n; i += S::NT) as[i] = p.alpha[base + t0 + i];
         __syncthreads();
-#pragma unroll 4
+#pragma unroll 2
         for (int t = 0; t < n; ++t) {
-            const float a = as[t], v = vs[t][cl];
+            const float a = as[t];
+            float v[CW], acc[CW];
+            if constexpr (CW == 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(&vs[t][cl]);
+                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+            } else {
+                v[0] = vs[t][cl];
+            }
+#pragma unroll
+            for (int c = 0; c < CW; ++c) acc[c] = 0.f;
             if (SUMS) upto *= a;
-            float acc = 0.f;
 #pragma unroll
             for (int i = 0; i < S::RW; i += 4) {
                 const float4 k4 = *reinterpret_cast<const float4 *>(&ks[t][(i / 4 * S::SL + r) * 4]);
-                s[i] = fmaf(a, s[i], k4.x * v);
-                s[i + 1] = fmaf(a, s[i + 1], k4.y * v);
-                s[i + 2] = fmaf(a, s[i + 2], k4.z * v);
-                s[i + 3] = fmaf(a, s[i + 3], k4.w * v);
+                const float kk[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int c = 0; c < CW; ++c) s[i + e][c] = fmaf(a, s[i + e][c], kk[e] * v[c]);
                 if constexpr (!SUMS) {
                     const float4 q4 = *reinterpret_cast<const float4 *>(&qs[t][(i / 4 * S::SL + r) * 4]);
-                    acc = fmaf(q4.x, s[i], acc);
-                    acc = fmaf(q4.y, s[i + 1], acc);
-                    acc = fmaf(q4.z, s[i + 2], acc);
-                    acc = fmaf(q4.w, s[i + 3], acc);
+                    const float qq[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int c = 0; c < CW; ++c) acc[c] = fmaf(qq[e], s[i + e][c], acc[c]);
                 }
             }
-            if constexpr (!SUMS) {
+            if constexpr (!SUMS && CW == 1) {
 #pragma unroll
-                for (int m = S::SL / 2; m > 0; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
-                if (r == 0) os[t][cl] = acc;
+                for (int m = S::SL / 2; m > 0; m >>= 1) acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], m);
+                if (r == 0) os[t][cl] = acc[0];
+            }
+            if constexpr (!SUMS && CW == 4) {
+                // four sums over eight lanes: a lane keeps half of its columns at a step
+                const bool hi = r & 4, odd = r & 2;
+                float x = hi ? acc[2] : acc[0], y = hi ? acc[3] : acc[1];
+                x += __shfl_xor_sync(0xffffffffu, hi ? acc[0] : acc[2], 4);
+                y += __shfl_xor_sync(0xffffffffu, hi ? acc[1] : acc[3], 4);
+                float z = odd ? y : x;
+                z += __shfl_xor_sync(0xffffffffu, odd ? x : y, 2);
+                z += __shfl_xor_sync(0xffffffffu, z, 1);
+                if (!(r & 1)) os[t][cl + (r >> 1)] = z;
             }
         }
         __syncthreads();
         if constexpr (SUMS) continue;
         float bad = 0.f;
-        for (int i = tid; i < n * S::CB; i += S::NT) {
-            const float x = os[i / S::CB][i % S::CB];
-            bad += x - x;
-            p.o[(base + t0 + i / S::CB) * D + c0 + i % S::CB] = x;
+        for (int i = 4 * tid; i < n * S::CB; i += 4 * S::NT) {
+            const float4 x = *reinterpret_cast<const float4 *>(&os[0][0] + i);
+            bad += (x.x - x.x) + (x.y - x.y) + (x.z - x.z) + (x.w - x.w);
+            *reinterpret_cast<float4 *>(p.o + (base + t0 + i / S::CB) * D + c0 + i % S::CB) = x;
         }
         if (bad != 0.f) flag(p.status, kFlagNonfinite);
         // os is next written behind the next block's staging barrier, so no third barrier is needed
@@ -194,10 +221,12 @@ __global__ void __launch_bounds__(SerialCfg<D>::NT) decay_serial_kernel(const De
     if (!SUMS && end != len) return;
     float *to = SUMS ? record : pool, bad = 0.f;
 #pragma unroll
-    for (int i = 0; i < S::RW; ++i) {
-        to[(size_t)((i / 4 * S::SL + r) * 4 + i % 4) * D] = s[i];
-        bad += s[i] - s[i];
-    }
+    for (int i = 0; i < S::RW; ++i)
+#pragma unroll
+        for (int c = 0; c < CW; ++c) {
+            to[row(i) + c] = s[i][c];
+            bad += s[i][c] - s[i][c];
+        }
     if (bad != 0.f) flag(p.status, kFlagNonfinite);
     if (SUMS && tid == 0 && c0 == 0) p.products[tile * p.segments + seg] = (float)upto;
 }
@@ -248,17 +277,32 @@ cudaError_t step(const DecayParams &p, int in_bf16, cudaStream_t s)
     return cudaGetLastError();
 }
 
-template <int D, int IN_BF16>
+template <int D, int IN_BF16, int CW>
 cudaError_t serial(const DecayParams &p, bool sums, cudaStream_t s)
 {
+    using S = SerialCfg<D, CW>;
     const size_t tiles = (size_t)p.B * p.H;
     const unsigned gy = (unsigned)(tiles < 32768 ? tiles : 32768);
-    const dim3 grid((unsigned)p.segments * (D / SerialCfg<D>::CB), gy, (unsigned)((tiles + gy - 1) / gy));
+    const dim3 grid((unsigned)p.segments * (D / S::CB), gy, (unsigned)((tiles + gy - 1) / gy));
     if (sums)
-        decay_serial_kernel<D, IN_BF16, 1><<<grid, SerialCfg<D>::NT, 0, s>>>(p);
+        decay_serial_kernel<D, IN_BF16, 1, CW><<<grid, S::NT, 0, s>>>(p);
     else
-        decay_serial_kernel<D, IN_BF16, 0><<<grid, SerialCfg<D>::NT, 0, s>>>(p);
+        decay_serial_kernel<D, IN_BF16, 0, CW><<<grid, S::NT, 0, s>>>(p);
     return cudaGetLastError();
+}
+
+template <int D, int CW>
+cudaError_t serial(const DecayParams &p, int in_bf16, bool sums, cudaStream_t s)
+{
+    return in_bf16 ? serial<D, 1, CW>(p, sums, s) : serial<D, 0, CW>(p, sums, s);
+}
+
+// Four columns to a thread feed the FMAs from a quarter of the shared memory's reads, one to a thread
+// makes four times the warps. 32 heads of 2048 tokens of d = 128: 284 us with four, 479 with one; 4 heads of
+// 500 tokens of d = 64: 44 and 34 us.
+bool serial_wide(const DecayParams &p, int d)
+{
+    return (int64_t)p.B * p.H * p.segments * d > 148 * 128;
 }
 
 cudaError_t decay_join(const DecayParams &p, int d, cudaStream_t s)
@@ -279,7 +323,10 @@ constexpr int kMostSegments = 1024;  // the join goes along them
 
 Split split(int B, int H, int T, int d, int in_bf16, bool cut)
 {
-    Split r{in_bf16 && T >= 64, 1, T};
+    // A chunk takes its time however few of its tokens there are. 512 heads of bf16, chunk against token by
+    // token: d = 128 at 32 tokens 54 and 58 us, d = 64 at 64 tokens 33 and 34 us, d = 32 at 100 tokens 31 and
+    // 32 us; 8 heads of d = 16 at 200 tokens 13 and 28 us.
+    Split r{in_bf16 && ((int64_t)T * d >= 4096 || T >= 128), 1, T};
     const int64_t tiles = (int64_t)B * H;
     if (r.chunk) {
         // One CTA to an SM: rounds of CTAs, each its chunks and 3.5 chunks' time of start and end (20 us; 5.5
@@ -299,9 +346,11 @@ Split split(int B, int H, int T, int d, int in_bf16, bool cut)
         r.seg_tokens = (int)(per * kDecayChunk < 0x7fffffff ? per * kDecayChunk : 0x7fffff80);
         return r;
     }
-    const int64_t ctas = tiles * (d > 32 ? d / 32 : 1);
-    if (!cut || T < 128 || ctas > 2 * kSMs) return r;
-    int64_t n = 6 * kSMs / ctas;
+    const int64_t ctas = tiles * (d > 64 ? d / 64 : 1);
+    // CTAs to an SM (512 heads of 1024 tokens of d = 16: 165 us with 4, 152 with 8, 119 with 12)
+    const int64_t want = d <= 32 ? 12 : 8;
+    if (!cut || T < 128 || ctas > want * kSMs / 2) return r;
+    int64_t n = want * kSMs / ctas;
     n = n < T / 64 ? n : T / 64;
     n = n < kMostSegments ? n : kMostSegments;
     const int64_t per = (((int64_t)T + n - 1) / n + 31) / 32 * 32;
@@ -319,11 +368,12 @@ size_t split_bytes(const Split &r, int B, int H, int d)
 
 cudaError_t launch_decay_serial(const DecayParams &p, int d, int in_bf16, bool sums, cudaStream_t s)
 {
+    const bool wide = serial_wide(p, d);
     switch (d) {
-        case 16: return in_bf16 ? serial<16, 1>(p, sums, s) : serial<16, 0>(p, sums, s);
-        case 32: return in_bf16 ? serial<32, 1>(p, sums, s) : serial<32, 0>(p, sums, s);
-        case 64: return in_bf16 ? serial<64, 1>(p, sums, s) : serial<64, 0>(p, sums, s);
-        default: return in_bf16 ? serial<128, 1>(p, sums, s) : serial<128, 0>(p, sums, s);
+        case 16: return serial<16, 1>(p, in_bf16, sums, s);
+        case 32: return wide ? serial<32, 4>(p, in_bf16, sums, s) : serial<32, 1>(p, in_bf16, sums, s);
+        case 64: return wide ? serial<64, 4>(p, in_bf16, sums, s) : serial<64, 1>(p, in_bf16, sums, s);
+        default: return wide ? serial<128, 4>(p, in_bf16, sums, s) : serial<128, 1>(p, in_bf16, sums, s);
     }
 }
 

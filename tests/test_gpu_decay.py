@@ -297,3 +297,74 @@ def test_states_park_as_codes(stq):
     c = (S * S).mean(dim=2, keepdim=True).sqrt()
     r = (S / c).abs().amax(dim=3, keepdim=True) / 127
     assert torch.all((S - back).abs() <= r * c * (0.5 + 1e-3))
+
+
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+@pytest.mark.parametrize("lens", [None, [3000, 1, 0, 129, 2999]])
+def test_prefill_segments_of_full_precision_prompts(stq, d, lens):
+    """Long float32 prompts of few heads are cut into segments; ends in, at and between their borders."""
+    B = 1 if lens is None else len(lens)
+    need = stq.decay_prefill_workspace_bytes(B, 2, 3000, d, torch.float32)
+    assert need > 0
+    check(stq, B, 2, 3000, d, torch.float32, lens=lens, half=300.0, seed=21)
+    check(stq, B, 2, 3000, d, torch.float32, lens=lens, half=300.0, seed=21, ws=False)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_prefill_many_heads(stq, d, kind):
+    """As many heads as take four columns to a thread token by token, short and ragged."""
+    check(stq, 20, 32, 40, d, kind, lens=[40 - 2 * b for b in range(20)], seed=22)
+
+
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+def test_prefill_ends_inside_a_warps_rows(stq, d):
+    """Chunks whose last tokens fill some of the 32-row groups of o, whole or in part."""
+    check(stq, 7, 2, 256, d, torch.bfloat16, lens=[32, 33, 63, 64, 160, 191, 255], seed=23)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d", [16, 128])
+def test_prefill_cleared_at_borders(stq, d, kind):
+    """Decays of zero at the first and last tokens of chunks and groups, over several segments."""
+    def mutate(q, k, v, alpha, states):
+        for t in (0, 15, 16, 127, 128, 255, 256, 1023, 1024, 1999):
+            alpha[:, 0, t] = 0.0
+
+    check(stq, 1, 2, 2000, d, kind, mutate=mutate, half=2000.0, seed=24)
+
+
+def test_two_prompts_at_once(stq):
+    """Two prompts on two streams, each with its workspace, do what they do alone."""
+    B, H, T, d = 1, 3, 4000, 128
+    runs = []
+    for seed in (31, 32):
+        q, k, v, alpha, slots, states = (x.to(DEV) for x in make(B, H, T, d, torch.bfloat16, seed=seed))
+        need = stq.decay_prefill_workspace_bytes(B, H, T, d, torch.bfloat16)
+        st, o = states.clone(), torch.empty(B, H, T, d, device=DEV)
+        stq.decay_prefill(st, slots, q, k, v, alpha, o, workspace=torch.empty(need, dtype=torch.uint8, device=DEV))
+        runs.append((q, k, v, alpha, slots, states, st, o, torch.empty(need, dtype=torch.uint8, device=DEV), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    out = []
+    for _ in range(3):
+        for q, k, v, alpha, slots, states, st, o, ws, s in runs:
+            with torch.cuda.stream(s):
+                st2, o2 = states.clone(), torch.empty_like(o)
+                stq.decay_prefill(st2, slots, q, k, v, alpha, o2, workspace=ws)
+                out.append((st, st2, o, o2))
+    torch.cuda.synchronize()
+    for st, st2, o, o2 in out:
+        assert torch.equal(st, st2) and torch.equal(o, o2)
+
+
+def test_status_flags_name_no_wait_that_ran_out(stq):
+    """A second of prompts of every shape back to back: no bounded wait gives up."""
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for i, (B, H, T, d) in enumerate([(1, 1, 1, 128), (3, 7, 4097, 128), (2, 40, 513, 64), (1, 5, 2049, 16), (9, 9, 129, 32)]):
+        q, k, v, alpha, slots, states = (x.to(DEV) for x in make(B, H, T, d, torch.bfloat16, seed=40 + i))
+        need = stq.decay_prefill_workspace_bytes(B, H, T, d, torch.bfloat16)
+        ws = torch.empty(need, dtype=torch.uint8, device=DEV) if need else None
+        o = torch.empty(B, H, T, d, device=DEV)
+        for _ in range(40):
+            stq.decay_prefill(states, slots, q, k, v, alpha, o, workspace=ws, status=status)
+    assert status.item() == 0, stq.status_flags(status)
