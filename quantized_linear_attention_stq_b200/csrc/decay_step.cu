@@ -23,17 +23,29 @@
 namespace stq {
 namespace {
 
+// Four inputs as they lie in memory.
 template <int IN_BF16>
-__device__ __forceinline__ float4 load_in4(const void *base, size_t idx)
-{
-    if constexpr (IN_BF16) {
-        const uint2 r = *reinterpret_cast<const uint2 *>(reinterpret_cast<const __nv_bfloat16 *>(base) + idx);
+struct Raw4 {
+    uint2 r;
+    __device__ __forceinline__ void load(const void *base, size_t idx)
+    {
+        r = *reinterpret_cast<const uint2 *>(reinterpret_cast<const __nv_bfloat16 *>(base) + idx);
+    }
+    __device__ __forceinline__ float4 value() const
+    {
         return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u), __uint_as_float(r.y << 16),
                            __uint_as_float(r.y & 0xFFFF0000u));
-    } else {
-        return *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(base) + idx);
     }
-}
+};
+template <>
+struct Raw4<0> {
+    float4 r;
+    __device__ __forceinline__ void load(const void *base, size_t idx)
+    {
+        r = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(base) + idx);
+    }
+    __device__ __forceinline__ float4 value() const { return r; }
+};
 
 template <int D>
 struct StepCfg {
@@ -65,7 +77,9 @@ __global__ void __launch_bounds__(StepCfg<D>::NT) decay_step_kernel(const DecayP
         qs[i] = load_in<IN_BF16>(p.q, tile * D + i);
         ks[i] = load_in<IN_BF16>(p.k, tile * D + i);
     }
-    const float4 v = load_in4<IN_BF16>(p.v, tile * D + 4 * c);
+    Raw4<IN_BF16> rv;
+    rv.load(p.v, tile * D + 4 * c);
+    const float4 v = rv.value();
     const float a = p.alpha[tile];
     __syncthreads();
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -112,7 +126,7 @@ struct SerialCfg {
     static constexpr int RW = D / SL;                              // rows of a thread
     static constexpr int CB = CW == 1 ? (D < 32 ? D : 32) : (D < 64 ? D : 64);  // columns of a CTA
     static constexpr int NT = CB / CW * SL;
-    static constexpr int TB = CW == 1 ? 32 : 16;                   // tokens staged at a time
+    static constexpr int TB = D < 32 ? 32 : 16;                              // tokens staged at a time
 };
 
 template <int D, int IN_BF16, int SUMS, int CW>
@@ -120,7 +134,10 @@ __global__ void __launch_bounds__(SerialCfg<D, CW>::NT) decay_serial_kernel(cons
 {
     using S = SerialCfg<D, CW>;
     __shared__ __align__(16) float qs[SUMS ? 1 : S::TB][D], ks[S::TB][D];
-    __shared__ __align__(16) float vs[S::TB][S::CB], os[S::TB][S::CB];
+    // with one column to a thread o is summed behind the tokens, from a part of every lane (a pitch of SL + 1
+    // keeps the lanes' writes and reads on different banks)
+    constexpr int PARTS = CW == 1 && !SUMS ? S::SL + 1 : 1;
+    __shared__ __align__(16) float vs[S::TB][S::CB], os[S::TB][S::CB * PARTS];
     __shared__ float as[S::TB];
     const int tid = threadIdx.x, r = tid % S::SL, cl = tid / S::SL * CW;
     const int seg = blockIdx.x / (D / S::CB), c0 = blockIdx.x % (D / S::CB) * S::CB;
@@ -149,18 +166,48 @@ __global__ void __launch_bounds__(SerialCfg<D, CW>::NT) decay_serial_kernel(cons
         for (int c = 0; c < CW; ++c) s[i][c] = SUMS ? 0.f : before[row(i) + c];
     const size_t base = tile * (size_t)p.T;
     double upto = 1.0;
+    // a block's inputs are loaded a block ahead
+    constexpr int NQ = (S::TB * D / 4 + S::NT - 1) / S::NT, NV = (S::TB * S::CB / 4 + S::NT - 1) / S::NT;
+    static_assert(S::TB <= S::NT, "a thread has one decay of a block at most");
+    Raw4<IN_BF16> rq[NQ], rk[NQ], rv[NV];
+    float ra = 1.f;
+    auto fetch = [&](int t0) {
+        const int n = end - t0 < S::TB ? end - t0 : S::TB;
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) {
+            const int i = 4 * (tid + x * S::NT);
+            if (i < n * D) {
+                if (!SUMS) rq[x].load(p.q, (base + t0) * D + i);
+                rk[x].load(p.k, (base + t0) * D + i);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < NV; ++x) {
+            const int i = 4 * (tid + x * S::NT);
+            if (i < n * S::CB) rv[x].load(p.v, (base + t0 + i / S::CB) * D + c0 + i % S::CB);
+        }
+        if (tid < n) ra = p.alpha[base + t0 + tid];
+    };
+    fetch((int)from);
     for (int t0 = (int)from; t0 < end; t0 += S::TB) {
         const int n = end - t0 < S::TB ? end - t0 : S::TB;
-        for (int i = 4 * tid; i < n * D; i += 4 * S::NT) {
-            if (!SUMS) *reinterpret_cast<float4 *>(&qs[0][0] + i) = load_in4<IN_BF16>(p.q, (base + t0) * D + i);
-            *reinterpret_cast<float4 *>(&ks[0][0] + i) = load_in4<IN_BF16>(p.k, (base + t0) * D + i);
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) {
+            const int i = 4 * (tid + x * S::NT);
+            if (i < n * D) {
+                if (!SUMS) *reinterpret_cast<float4 *>(&qs[0][0] + i) = rq[x].value();
+                *reinterpret_cast<float4 *>(&ks[0][0] + i) = rk[x].value();
+            }
         }
-        for (int i = 4 * tid; i < n * S::CB; i += 4 * S::NT)
-            *reinterpret_cast<float4 *>(&vs[0][0] + i) =
-                load_in4<IN_BF16>(p.v, (base + t0 + i / S::CB) * D + c0 + i % S::CB);
-        for (int i = tid; i < n; i += S::NT) as[i] = p.alpha[base + t0 + i];
+#pragma unroll
+        for (int x = 0; x < NV; ++x) {
+            const int i = 4 * (tid + x * S::NT);
+            if (i < n * S::CB) *reinterpret_cast<float4 *>(&vs[0][0] + i) = rv[x].value();
+        }
+        if (tid < n) as[tid] = ra;
+        if (end - t0 > S::TB) fetch(t0 + S::TB);
         __syncthreads();
-#pragma unroll 2
+#pragma unroll(CW == 1 ? 8 : 2)
         for (int t = 0; t < n; ++t) {
             const float a = as[t];
             float v[CW], acc[CW];
@@ -190,11 +237,7 @@ __global__ void __launch_bounds__(SerialCfg<D, CW>::NT) decay_serial_kernel(cons
                         for (int c = 0; c < CW; ++c) acc[c] = fmaf(qq[e], s[i + e][c], acc[c]);
                 }
             }
-            if constexpr (!SUMS && CW == 1) {
-#pragma unroll
-                for (int m = S::SL / 2; m > 0; m >>= 1) acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], m);
-                if (r == 0) os[t][cl] = acc[0];
-            }
+            if constexpr (!SUMS && CW == 1) os[t][cl * PARTS + r] = acc[0];
             if constexpr (!SUMS && CW == 4) {
                 // four sums over eight lanes: a lane keeps half of its columns at a step
                 const bool hi = r & 4, odd = r & 2;
@@ -211,7 +254,19 @@ __global__ void __launch_bounds__(SerialCfg<D, CW>::NT) decay_serial_kernel(cons
         if constexpr (SUMS) continue;
         float bad = 0.f;
         for (int i = 4 * tid; i < n * S::CB; i += 4 * S::NT) {
-            const float4 x = *reinterpret_cast<const float4 *>(&os[0][0] + i);
+            float4 x;
+            if constexpr (CW == 4) {
+                x = *reinterpret_cast<const float4 *>(&os[0][0] + i);
+            } else {
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float *part = &os[0][0] + (i + e) * PARTS;
+                    y[e] = part[0] + part[1] + (part[2] + part[3]);
+                    if constexpr (S::SL == 8) y[e] += part[4] + part[5] + (part[6] + part[7]);
+                }
+                x = make_float4(y[0], y[1], y[2], y[3]);
+            }
             bad += (x.x - x.x) + (x.y - x.y) + (x.z - x.z) + (x.w - x.w);
             *reinterpret_cast<float4 *>(p.o + (base + t0 + i / S::CB) * D + c0 + i % S::CB) = x;
         }
