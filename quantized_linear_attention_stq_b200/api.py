@@ -337,8 +337,32 @@ def row_impact(q, k, beta, alpha, gate: int = GATE_SCALAR, stream=None) -> torch
 
 # --------------------------------------------------------------------------------------------
 # The layers next to the quantized ones: decayed linear attention, paged cache and attention.
-# These calls run on the device of their tensors, whatever the current one is.
+# These calls run on the device of their tensors, whatever the current one is. Each goes through the compiled
+# module first, which takes the usual case (csrc/binding.cpp); what follows here knows the others.
 # --------------------------------------------------------------------------------------------
+_native = None
+
+
+def _load():
+    """The compiled module (raises if it has not been built)."""
+    global _native
+    lib()
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise ImportError(f"_binding.so is missing or was built for another torch ({e}): build it with "
+                          "`python -m quantized_linear_attention_stq_b200.build`") from e
+    _native = _binding
+    return _binding
+
+
+def _done(st: int, what: str) -> bool:
+    """Whether the compiled module made the call; raises where the library refused it."""
+    if st > STQ_OK:
+        raise StqError(st, what)
+    return st == STQ_OK
+
+
 def _call(fn, what: str, dev: torch.device, status, stream, *args):
     """fn(*args, status, stream) with `dev` current and its current stream where none is given."""
     if dev.type != "cuda":
@@ -395,6 +419,8 @@ def decay_step(states, slots, q, k, v, alpha, o, status=None, stream=None):
 
     states [slots, H, d, d] fp32, slots [B] int32, q, k, v [B, H, d] (float32 or bfloat16), alpha
     [B, H] fp32, o [B, H, d] fp32. See stq_decay_step in include/stq.h."""
+    if _done((_native or _load()).decay_step(states, slots, q, k, v, alpha, o, status, stream), "stq_decay_step"):
+        return
     if isinstance(q, torch.Tensor) and q.dim() != 3:
         raise ValueError("q must be [B, H, d]")
     code, dev = _decay_args(states, slots, q, k, v, alpha, o)
@@ -414,6 +440,9 @@ def decay_prefill(states, slots, q, k, v, alpha, o, lens=None, workspace=None, s
     """decay_step over prompts: q, k, v [B, H, T, d], alpha [B, H, T], o [B, H, T, d] fp32, lens [B]
     int32 (tokens of each prompt; rows behind them are left alone) or None for T. See
     stq_decay_prefill in include/stq.h."""
+    if _done((_native or _load()).decay_prefill(states, slots, q, k, v, alpha, o, lens, workspace, status, stream),
+             "stq_decay_prefill"):
+        return
     if isinstance(q, torch.Tensor) and q.dim() != 4:
         raise ValueError("q must be [B, H, T, d]")
     code, dev = _decay_args(states, slots, q, k, v, alpha, o)
@@ -431,6 +460,9 @@ def page_plan(table, lens, fresh, free_pages, free_head, slot_map, starts, lens_
     """Pages, table entries and slots of the fresh[b] new tokens of requests that hold lens[b], from
     the free list (all int32 tensors; lens_out and head_out may be lens and free_head themselves).
     See stq_page_plan in include/stq.h."""
+    if _done((_native or _load()).page_plan(table, lens, fresh, free_pages, free_head, slot_map, starts, lens_out,
+                                            head_out, page_size, status, stream), "stq_page_plan"):
+        return
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("table must be a [B, width] tensor")
     dev, (B, W) = table.device, table.shape
@@ -462,6 +494,8 @@ def page_write(k_pages, v_pages, slot_map, k, v, status=None, stream=None):
     """Write new tokens' keys and values [N, kv_heads, d] to their slots of the paged cache
     [pages, kv_heads, page_size, d]; slot -1 skips a token. k and v may be strided over tokens. See
     stq_page_write in include/stq.h."""
+    if _done((_native or _load()).page_write(k_pages, v_pages, slot_map, k, v, status, stream), "stq_page_write"):
+        return
     code = _dtype(k, "k")
     if k.dim() != 3:
         raise ValueError("k must be [N, kv_heads, d]")
@@ -489,6 +523,9 @@ def paged_attention(q, k_pages, v_pages, table, lens, o, scale: float, workspace
     """Attention of one new token per request, q [B, q_heads, d], over the lens[b] cached tokens of
     its table row; o [B, q_heads, d] fp32. With a workspace the cache is split over the GPU. See
     stq_paged_attention in include/stq.h."""
+    if _done((_native or _load()).paged_attention(q, k_pages, v_pages, table, lens, o, scale, workspace, status,
+                                                  stream), "stq_paged_attention"):
+        return
     code = _dtype(q, "q")
     if q.dim() != 3:
         raise ValueError("q must be [B, q_heads, d]")

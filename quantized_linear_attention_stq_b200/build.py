@@ -1,4 +1,5 @@
-"""Build the CUDA library in-tree: csrc/*.cu -> libstq.so (sm_100a only).
+"""Build the CUDA library in-tree: csrc/*.cu -> libstq.so (sm_100a only), and the binding's usual case:
+csrc/binding.cpp -> _binding.so (host code against the installed torch).
 
 ``python -m quantized_linear_attention_stq_b200.build`` or ``build()`` from Python. The library
 is rebuilt when a source or the public header is newer than the shared object.
@@ -10,12 +11,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 HEADER = os.path.join(ROOT, "include", "stq.h")
 LIB = os.path.join(PKG, "libstq.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -40,6 +43,31 @@ def stale() -> bool:
     return os.path.getmtime(LIB) < max(os.path.getmtime(f) for f in deps)
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """Compile _binding.so where its source or the public header is newer."""
+    src = os.path.join(CSRC, "binding.cpp")
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, (src, HEADER))):
+        return BINDING
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    includes = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"), cuda,
+                sysconfig.get_paths()["include"]]
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-isystem{i}" for i in includes], "-o",
+           tmp, src, "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-L" + PKG,
+           "-l:libstq.so", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    proc = subprocess.run(cmd, capture_output=True, text=True)
+    if proc.returncode != 0:
+        raise RuntimeError(f"g++ failed on {src} ({proc.returncode}):\n{proc.stdout}\n{proc.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def _compile(src: str, obj: str, ptxas_info: bool):
     cmd = [_nvcc(), *ARCH, *FLAGS, "-c", "-o", obj, src]
     if ptxas_info:
@@ -52,6 +80,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     """Compile every source to an object (in parallel, under the package's _build folder), then
     link libstq.so. Objects whose source and headers are older than them are reused."""
     if not (force or stale()):
+        build_binding(force, verbose)
         return LIB
     from concurrent.futures import ThreadPoolExecutor
 
@@ -80,6 +109,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if proc.returncode != 0:
         raise RuntimeError(f"nvcc link failed ({proc.returncode}):\n{proc.stdout}\n{proc.stderr}")
     os.replace(tmp, LIB)
+    build_binding(force, verbose)
     return LIB
 
 

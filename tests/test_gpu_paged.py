@@ -475,3 +475,47 @@ def test_two_streams_at_once(stq):
             stq.paged_attention(q, kp, vp, table, lens, o, 0.1, workspace=w, stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(alone, both))
+
+
+def test_compiled_binding_and_python_make_the_same_calls(stq):
+    """A tensor subclass and a stream argument go the Python way: the same outputs, bit for bit, and the same
+    refusals."""
+    from quantized_linear_attention_stq_b200 import _binding as b
+
+    class Sub(torch.Tensor):
+        pass
+
+    g = torch.Generator(device=DEV).manual_seed(3)
+    rnd = lambda *s: torch.randn(s, generator=g, device=DEV)  # noqa: E731
+    side = torch.cuda.Stream()
+    N, H, d, page, n = 9, 1, 32, 4, 5
+    both = rnd(N, 2 * H * d)
+    k, v = (x.view(N, H, d) for x in both.split(H * d, dim=1))
+    slots = torch.randperm(n * page, generator=g, device=DEV)[:N].to(torch.int32)
+    pages = [torch.zeros(n, H, page, d, device=DEV) for _ in range(6)]
+    assert b.page_write(pages[0], pages[1], slots, k, v, None, None) == 0
+    assert b.page_write(pages[2], pages[3], slots, k.as_subclass(Sub), v, None, None) == -1
+    stq.page_write(pages[2], pages[3], slots, k.as_subclass(Sub), v)
+    torch.cuda.synchronize()
+    stq.page_write(pages[4], pages[5], slots, k, v, stream=side)
+    side.synchronize()
+    for x in pages[2:]:
+        assert torch.equal(x, pages[0] if torch.equal(x, pages[0]) else pages[1])
+    assert torch.equal(pages[0], pages[2]) and torch.equal(pages[1], pages[5])
+    q = rnd(2, 4, d)
+    table = torch.tensor([[1, 0, 2], [3, 4, 0]], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([11, 7], dtype=torch.int32, device=DEV)
+    out = [torch.empty(2, 4, d, device=DEV) for _ in range(2)]
+    ws = torch.empty(stq.paged_attention_workspace_bytes(2, 4, d, H), dtype=torch.uint8, device=DEV)
+    assert b.paged_attention(q, pages[0], pages[1], table, lens, out[0], 0.3, ws, None, None) == 0
+    torch.cuda.synchronize()
+    stq.paged_attention(q.as_subclass(Sub), pages[0], pages[1], table, lens, out[1], 0.3, workspace=ws)
+    assert torch.equal(out[0], out[1])
+    # a workspace that is too small is not taken by the compiled call, and named by the Python one
+    assert b.paged_attention(q, pages[0], pages[1], table, lens, out[0], 0.3, ws[:64], None, None) == -1
+    with pytest.raises(ValueError):
+        stq.paged_attention(q, pages[0], pages[1], table, lens, out[0], 0.3, workspace=ws[:64])
+    # what the library refuses is raised from either way
+    for x in (q, q.as_subclass(Sub)):
+        with pytest.raises(stq.StqError):
+            stq.paged_attention(x, pages[0], pages[1], table, lens, out[0], float("inf"), workspace=ws)

@@ -146,3 +146,32 @@ def test_binding_checks(stq):
                 dict(head_out=z(2, t=i))):
         with pytest.raises(ValueError):
             stq.page_plan(**{**pl, **bad})
+
+
+def test_compiled_binding_leaves_the_unusual_to_python(stq):
+    """The compiled module answers -1, without a call, to all that is not a contiguous CUDA tensor of the
+    expected kind, and Python then says what is wrong."""
+    from quantized_linear_attention_stq_b200 import _binding as b
+
+    z = lambda *s, t=torch.float32: torch.zeros(*s, dtype=t)  # noqa: E731
+    i = torch.int32
+    step = [z(3, 2, 16, 16), z(1, t=i), z(1, 2, 16), z(1, 2, 16), z(1, 2, 16), z(1, 2), z(1, 2, 16), None, None]
+    calls = {
+        "decay_step": step,
+        "decay_prefill": [step[0], step[1]] + [z(1, 2, 4, 16)] * 3 + [z(1, 2, 4), z(1, 2, 4, 16), None, None, None, None],
+        "page_plan": [z(1, 2, t=i), z(1, t=i), z(1, t=i), z(4, t=i), z(1, t=i), z(3, t=i), z(2, t=i), z(1, t=i), z(1, t=i),
+                      16, None, None],
+        "page_write": [z(2, 1, 4, 16), z(2, 1, 4, 16), z(3, t=i), z(3, 1, 16), z(3, 1, 16), None, None],
+        "paged_attention": [z(1, 2, 16), z(2, 1, 4, 16), z(2, 1, 4, 16), z(1, 2, t=i), z(1, t=i), z(1, 2, 16), 1.0, None,
+                            None, None],
+    }
+    for name, args in calls.items():
+        f = getattr(b, name)
+        assert f(*args) == -1, name
+        for n in range(len(args)):
+            assert f(*args[:n], "x", *args[n + 1:]) == -1
+            assert f(*args[:n], None, *args[n + 1:]) == -1
+        with pytest.raises(TypeError):
+            f(*args, None)
+        with pytest.raises(TypeError):
+            f()
