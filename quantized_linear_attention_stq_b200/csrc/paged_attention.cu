@@ -102,17 +102,23 @@ __device__ __forceinline__ Cursor find_share(const Params &p, int units)
 template <int D, int GT>
 struct SimtSmem {
     float q[GT][D];
-    float k[KT][D + 4];
-    float v[KT][D];
+    float k[2][KT][D + 4];
+    float v[2][KT][D];
+    long long at[3][KT];  // where a stage's keys stand; -1: none
     float s[4][GT][KT];  // partial scores of the four quarters of d
     float p[GT][KT];
     float corr[GT], m[GT], l[GT];
-    static_assert(KT * (D + 4) >= GT * D, "the joined sums fit where the keys were");
+    static_assert(2 * KT * (D + 4) >= GT * D, "the joined sums fit where the keys were");
 };
 
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+
 // One unit's tiles [t0, t1): scores by quarters of d (a lane per key, a warp per quarter), softmax
-// by rows, products by (columns, key class). Leaves the sums in acc, joined over the key classes, in
-// shared memory (sums[GT][D]), and m, l.
+// by rows, products by (columns, key class). Copies run a stage ahead, the look-up of the pages one
+// further. Leaves the sums in acc, joined over the key classes, in shared memory (sums[GT][D]), and m, l.
 template <int D, int GT>
 __device__ __forceinline__ void simt_unit(const Params &p, SimtSmem<D, GT> &sm, int b, int hk, int rt, int len,
                                           int t0, int t1, float *sums)
@@ -122,7 +128,36 @@ __device__ __forceinline__ void simt_unit(const Params &p, SimtSmem<D, GT> &sm, 
     const int c4 = tid % C4, part = tid / C4;
     const int rows = min(GT, p.group - rt * ROWS);
     const size_t q0 = ((size_t)b * p.Hq + (size_t)hk * p.group + rt * ROWS) * D;
+    const int32_t *row = p.table + (size_t)b * p.W;
+    const int first = t0 * TK, last = min(len, t1 * TK), N = (last - first + KT - 1) / KT;
+    auto look_up = [&](int n) {  // warp 0: the places of stage n's keys
+        const int t = first + n * KT + lane;
+        long long at = -1;
+        if (t < last) {
+            const int pg = row[t / p.page];
+            if (pg >= 0 && pg < p.num_pages)
+                at = (((long long)pg * p.Hkv + hk) * p.page + t % p.page) * D;
+            else
+                flag(p.status, kFlagBounds);
+        }
+        sm.at[n % 3][lane] = at;
+    };
+    auto copy = [&](int n) {
+#pragma unroll
+        for (int x = 0; x < KT * C4 / NTA; ++x) {
+            const int i = tid + x * NTA, r = i / C4, c = 4 * (i % C4);
+            const long long at = sm.at[n % 3][r];
+            const long long from = at < 0 ? 0 : at + c;
+            cp16(smem_u32(&sm.k[n & 1][r][c]), (const float *)p.k_pages + from, at >= 0);
+            cp16(smem_u32(&sm.v[n & 1][r][c]), (const float *)p.v_pages + from, at >= 0);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
     __syncthreads();  // the unit before has been read out
+    if (w == 0) {
+        look_up(0);
+        look_up(1);
+    }
     for (int i = tid; i < GT * D; i += NTA) (&sm.q[0][0])[i] = i < rows * D ? ((const float *)p.q)[q0 + i] : 0.f;
     if (tid < GT) {
         sm.m[tid] = -INFINITY;
@@ -133,30 +168,18 @@ __device__ __forceinline__ void simt_unit(const Params &p, SimtSmem<D, GT> &sm, 
     for (int g = 0; g < GT; ++g)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[g][e] = 0.f;
-    const int32_t *row = p.table + (size_t)b * p.W;
-    const int first = t0 * TK, last = min(len, t1 * TK);
-    for (int k0 = first; k0 < last; k0 += KT) {
-        __syncthreads();
-        for (int i = tid; i < KT * C4; i += NTA) {
-            const int r = i / C4, c = i % C4, t = k0 + r;
-            float4 kk = make_float4(0.f, 0.f, 0.f, 0.f), vv = kk;
-            float live = 0.f;
-            if (t < last) {
-                const int pg = row[t / p.page];
-                if (pg >= 0 && pg < p.num_pages) {
-                    const size_t at = (((size_t)pg * p.Hkv + hk) * p.page + t % p.page) * D + 4 * c;
-                    kk = *reinterpret_cast<const float4 *>((const float *)p.k_pages + at);
-                    vv = *reinterpret_cast<const float4 *>((const float *)p.v_pages + at);
-                    live = 1.f;
-                } else {
-                    flag(p.status, kFlagBounds);
-                }
-            }
-            *reinterpret_cast<float4 *>(&sm.k[r][4 * c]) = kk;
-            *reinterpret_cast<float4 *>(&sm.v[r][4 * c]) = vv;
-            if (c == 0) sm.k[r][D] = live;  // in the row's padding
+    __syncthreads();
+    copy(0);
+    for (int n = 0; n < N; ++n) {
+        if (n + 1 < N) {
+            copy(n + 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
         }
         __syncthreads();
+        const float(*ks)[D + 4] = sm.k[n & 1];
+        const float(*vs)[D] = sm.v[n & 1];
         {  // scores: lane = key, warp = quarter of d
             float s[GT];
 #pragma unroll
@@ -164,7 +187,7 @@ __device__ __forceinline__ void simt_unit(const Params &p, SimtSmem<D, GT> &sm, 
 #pragma unroll
             for (int c = 0; c < C4 / 4; ++c) {
                 const int col = (w * (C4 / 4) + c) * 4;
-                const float4 kk = *reinterpret_cast<const float4 *>(&sm.k[lane][col]);
+                const float4 kk = *reinterpret_cast<const float4 *>(&ks[lane][col]);
 #pragma unroll
                 for (int g = 0; g < GT; ++g) {
                     const float4 qq = *reinterpret_cast<const float4 *>(&sm.q[g][col]);
@@ -174,10 +197,11 @@ __device__ __forceinline__ void simt_unit(const Params &p, SimtSmem<D, GT> &sm, 
 #pragma unroll
             for (int g = 0; g < GT; ++g) sm.s[w][g][lane] = s[g];
         }
+        if (w == 0) look_up(n + 2);
         __syncthreads();
         for (int g = w; g < GT; g += NTA / 32) {
             float s = (sm.s[0][g][lane] + sm.s[1][g][lane]) + (sm.s[2][g][lane] + sm.s[3][g][lane]);
-            s = sm.k[lane][D] != 0.f ? s * p.scale2 : -INFINITY;
+            s = sm.at[n % 3][lane] >= 0 ? s * p.scale2 : -INFINITY;
             float top = s;
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -202,8 +226,9 @@ __device__ __forceinline__ void simt_unit(const Params &p, SimtSmem<D, GT> &sm, 
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[g][e] *= c;
         }
+#pragma unroll 4
         for (int r = part; r < KT; r += PARTS) {
-            const float4 vv = *reinterpret_cast<const float4 *>(&sm.v[r][4 * c4]);
+            const float4 vv = *reinterpret_cast<const float4 *>(&vs[r][4 * c4]);
 #pragma unroll
             for (int g = 0; g < GT; ++g) {
                 const float e = sm.p[g][r];
@@ -213,6 +238,7 @@ __device__ __forceinline__ void simt_unit(const Params &p, SimtSmem<D, GT> &sm, 
                 acc[g][3] = fmaf(e, vv.w, acc[g][3]);
             }
         }
+        __syncthreads();  // the stage is overwritten next
     }
     // join the key classes, one class at a time (a fixed order)
     for (int r = 0; r < PARTS; ++r) {
@@ -269,10 +295,6 @@ __device__ __forceinline__ uint32_t row_chunk(int r, int c)
     return (uint32_t)(r * CH + (c ^ ((r / PER) & MASK))) * 16u;
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a)
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -597,7 +619,7 @@ __global__ void __launch_bounds__(NTA) paged_simt_kernel(const Params p)
 {
     extern __shared__ __align__(16) uint8_t raw[];
     SimtSmem<D, GT> &sm = *reinterpret_cast<SimtSmem<D, GT> *>(raw);
-    float *sums = &sm.k[0][0];  // a unit's sums are joined where its keys were
+    float *sums = &sm.k[0][0][0];  // a unit's sums are joined where its keys were
     walk(p, [&](int b, int hk, int rt, int len, int t0, int t1, int piece) {
         simt_unit<D, GT>(p, sm, b, hk, rt, len, t0, t1, sums);
         finish<D>(p, b, hk, rt, sums, sm.m, sm.l, piece);
