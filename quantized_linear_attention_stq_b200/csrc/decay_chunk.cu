@@ -52,11 +52,12 @@ struct ChunkGates {
 };
 
 // Loads of q, k, v landed; k free; v free; gates made / free; scores done; P made; O done; P V done; o read; e K's slots full / free; dS done / read; S's terms made; end.
-enum { FQ, FK, FV = FK + 3, KE = FV + 3, VE = KE + 3, GA = VE + 3, GF, SC, PF, QS, OF, OFF, KTF, KTE = KTF + 8, DS = KTE + 8, DSF, SF, END, NBAR };
+enum { FQ, FK, FV = FK + 3, KE = FV + 3, VE = KE + 3, GA = VE + 3, GF = GA + 2, SC = GF + 2, PF, QS, OF, OFF, KTF, KTE = KTF + 8, DS = KTE + 8, DSF = DS + 2, SF = DSF + 2, END, NBAR };
 
+template <int STAGES>
 struct ChunkMisc {
     unsigned long long bars[NBAR];
-    alignas(16) ChunkGates g;
+    alignas(16) ChunkGates g[STAGES];
     uint32_t tmem;
 };
 
@@ -65,6 +66,7 @@ struct ChunkCfg {
     static constexpr uint32_t QB = KB * BOX;            // bytes of a q, k or v tile
     static constexpr int KS = SUMS ? 3 : 1;             // stages of k
     static constexpr int VS = SUMS ? 3 : 2;             // stages of v
+    static constexpr int GS = SUMS ? 2 : 1;             // stages of the decays' products, and dS's of columns
     static constexpr uint32_t K = 0;
     static constexpr uint32_t V = K + KS * QB;
     static constexpr uint32_t Q = V + VS * QB;
@@ -75,7 +77,7 @@ struct ChunkCfg {
     static constexpr uint32_t O = KB == 2 ? V : ST + (SUMS ? 0 : 3 * STB);
     static constexpr uint32_t OB = KB == 2 ? QB : 0;    // ... from one stage to the next
     static constexpr uint32_t MISC = ST + (SUMS ? 0 : 3 * STB) + (SUMS || KB == 2 ? 0 : 8 * 4096);
-    static constexpr uint32_t SMEM = MISC + sizeof(ChunkMisc);
+    static constexpr uint32_t SMEM = MISC + sizeof(ChunkMisc<GS>);
     static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
     static constexpr int SLOTS = SUMS ? 8 : 2;          // of e K
     static constexpr uint32_t KT = SUMS ? 0 : TM_KT;
@@ -234,10 +236,10 @@ __global__ void __launch_bounds__(NTC, 1)
                        const __grid_constant__ CUtensorMap mo)
 {
     using M = ChunkCfg<KB, SUMS>;
-    constexpr int KS = M::KS, VS = M::VS;
+    constexpr int KS = M::KS, VS = M::VS, GS = M::GS;
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
-    ChunkMisc &ms = *reinterpret_cast<ChunkMisc *>(sm + M::MISC);
+    ChunkMisc<M::GS> &ms = *reinterpret_cast<ChunkMisc<M::GS> *>(sm + M::MISC);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
     // (request, head), segment of the prompt
@@ -262,9 +264,9 @@ __global__ void __launch_bounds__(NTC, 1)
         for (int i = 0; i < NBAR; ++i) {
             int count = 1;
             if (i >= KE && i < KE + 3) count = SUMS ? 16 : 8;
-            if (i == GF) count = 24;
+            if (i >= GF && i < GF + 2) count = 24;
             if (i >= VE && i < VE + 3) count = SUMS ? 1 : 8;
-            if (i == PF || i == OFF || i == DSF || i == SF) count = 8;
+            if (i == PF || i == OFF || i == DSF || i == DSF + 1 || i == SF) count = 8;
             if (i >= KTF && i < KTF + 8) count = 4;
             mbar_init(bar(i), count);
         }
@@ -276,8 +278,8 @@ __global__ void __launch_bounds__(NTC, 1)
     umma::fence_after_sync();
     const uint32_t tmem = ms.tmem;
     const int quarter = warp & 3;
+    auto ds_at = [](int n) { return TM_DS - n % GS * 128; };  // dS's columns (sums have O's free)
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);  // this warp's lanes
-    const ChunkGates &g = ms.g;
     // a wait that gave up ends its role; the other roles' waits then give up too
     bool ok = true;
     auto wait = [&](int i, int phase) {  // of a warp
@@ -310,6 +312,7 @@ __global__ void __launch_bounds__(NTC, 1)
         if (quarter < 2 * KB) {
             const int tok = 16 * j + (lane & 7) + (lane >> 4) * 8, c8 = 4 * (quarter & 1) + (lane >> 3 & 1);
             const uint32_t k = sb + M::K + (n % KS) * M::QB + (quarter >> 1) * BOX;
+            const ChunkGates &g = ms.g[n % GS];
             const float2 e[2] = {*reinterpret_cast<const float2 *>(&g.e[16 * j + 2 * (lane & 3)]),
                                  *reinterpret_cast<const float2 *>(&g.e[16 * j + 8 + 2 * (lane & 3)])};
 #pragma unroll
@@ -355,7 +358,7 @@ __global__ void __launch_bounds__(NTC, 1)
     };
     // ... of groups j = first, first + step, ... of a chunk
     auto make_chunk = [&](int n, int first, int step) {
-        if (!wait(GA, n) || !wait(FK + n % KS, n / KS)) return;
+        if (!wait(GA + n % GS, n / GS) || !wait(FK + n % KS, n / KS)) return;
 #pragma unroll 1
         for (int j = first; j < 8 && ok; j += step) make_ek(n, j);
         if (ok) arrive(KE + n % KS);
@@ -367,7 +370,7 @@ __global__ void __launch_bounds__(NTC, 1)
         if constexpr (SUMS) {
             for (int n = 0; n < N && ok; ++n) {
                 make_chunk(n, warp >> 2, 4);
-                arrive(GF);
+                arrive(GF + n % GS);
             }
         } else {
             const int t = 32 * quarter + lane, sub = warp >> 2, l16 = lane & 15, top = 2 * quarter + 1;
@@ -379,6 +382,7 @@ __global__ void __launch_bounds__(NTC, 1)
             for (int n = 0; n < N; ++n) {
                 const int t0 = (n0 + n) * CT;
                 if (!wait(GA, n)) break;
+                const ChunkGates &g = ms.g[0];
                 const float bt = g.b[t], upto = g.upto[t];
                 if (!wait(SC, n)) break;
                 umma::fence_after_sync();
@@ -433,7 +437,7 @@ __global__ void __launch_bounds__(NTC, 1)
                 tmem_wait_st();
                 umma::fence_before_sync();
                 arrive(PF);
-                arrive(GF);
+                arrive(GF + n % GS);
                 if (n > 0) {  // the tile of the chunk before has left shared memory: v may be loaded there
                     if (lane == 0) tma_stores_read();
                     arrive(VE + (n - 1) % VS);
@@ -528,21 +532,21 @@ __global__ void __launch_bounds__(NTC, 1)
         double upto = 1.0;  // the segment's decay
         if (!SUMS) put_state();
         for (int n = 0; n < N && ok; ++n) {
-            if (!wait(GA, n)) break;
-            const float bc = (float)g.all;
-            upto *= g.all;
-            arrive(GF);
-            if (!wait(DS, n)) break;
+            if (!wait(GA + n % GS, n / GS)) break;
+            const float bc = (float)ms.g[n % GS].all;
+            upto *= ms.g[n % GS].all;
+            arrive(GF + n % GS);
+            if (!wait(DS + n % GS, n / GS)) break;
             umma::fence_after_sync();
 #pragma unroll
             for (int c = 0; c < SC_; c += 16) {
                 float x[16];
-                pf::tmem_ld16(tl + TM_DS + c0 + c, x);
+                pf::tmem_ld16(tl + ds_at(n) + c0 + c, x);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) S[c + e] = fmaf(bc, S[c + e], x[e]);
             }
             umma::fence_before_sync();
-            arrive(DSF);
+            arrive(DSF + n % GS);
             if (!SUMS && n + 1 < N) {
                 if (!wait(QS, n)) break;
                 put_state();
@@ -567,7 +571,7 @@ __global__ void __launch_bounds__(NTC, 1)
         for (int n = 0; n < N && ok; ++n) {
             const int x = warp >> 2 & 1;
             SUMS ? make_chunk(n, 2 + x, 4) : make_chunk(n, x, 2);
-            arrive(GF);
+            arrive(GF + n % GS);
         }
     } else if (regs_down<56>(); warp == 24) {
         // ---- TMA ----------------------------------------------------------------------------
@@ -625,7 +629,7 @@ __global__ void __launch_bounds__(NTC, 1)
                                            kn + (((kk >> 2) * BOX + (kk & 3) * 32) >> 4), id_sc, kk != 0);
                     umma::mma_commit(bar(SC));
                 }
-                if (!once(FV + n % VS, n / VS) || (n > 0 && !once(SUMS ? DSF : OFF, n - 1))) break;
+                if (!once(FV + n % VS, n / VS) || (n >= GS && !once(SUMS ? DSF + n % GS : OFF, n / GS - 1))) break;
                 auto o_step = [&](int kk) {
                     const uint64_t a = dq + (((kk >> 2) * BOX + (kk & 3) * 32) >> 4), s = ds + (kk * 2048 >> 4);
                     mma_same_a<0>(tmem + TM_O, a, s + (2 * M::STB >> 4), id_d, kk != 0);
@@ -640,9 +644,9 @@ __global__ void __launch_bounds__(NTC, 1)
                     umma::fence_after_sync();
                     const uint32_t a = tmem + M::KT + slot_ * KT_COLS;
                     const uint64_t v = vn + j * (2048 >> 4);
-                    mma_ts(tmem + TM_DS, a + 16, v, id_d, j != 0);
-                    mma_ts(tmem + TM_DS, a + 8, v, id_d, 1);
-                    mma_ts(tmem + TM_DS, a, v, id_d, 1);
+                    mma_ts(tmem + ds_at(n), a + 16, v, id_d, j != 0);
+                    mma_ts(tmem + ds_at(n), a + 8, v, id_d, 1);
+                    mma_ts(tmem + ds_at(n), a, v, id_d, 1);
                     umma::mma_commit(bar(KTE + slot_));
                     // Steps of O between the groups of dS: a slot's way back and forth takes longer than the other
                     // slot's products. The last steps are left for the time in which dS is read.
@@ -653,7 +657,7 @@ __global__ void __launch_bounds__(NTC, 1)
                     }
                 }
                 if (!ok) break;
-                umma::mma_commit(bar(DS));
+                umma::mma_commit(bar(DS + n % GS));
                 if constexpr (SUMS) {
                     umma::mma_commit(bar(VE + n % VS));
                 } else {
@@ -713,8 +717,8 @@ __global__ void __launch_bounds__(NTC, 1)
             right = __shfl_down_sync(0xffffffffu, right, 4);
             if (lane < 4) left = 1.0;
             if (lane >= 28) right = 1.0;
-            if (n >= 1 && !wait(GF, n - 1)) break;
-            ChunkGates &to = ms.g;
+            if (n >= GS && !wait(GF + n % GS, n / GS - 1)) break;
+            ChunkGates &to = ms.g[n % GS];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 pre *= a[i];
@@ -730,7 +734,7 @@ __global__ void __launch_bounds__(NTC, 1)
             }
             if ((lane & 3) == 0) to.group[lane >> 2] = (float)group;
             if (lane == 0) to.all = all;
-            arrive(GA);
+            arrive(GA + n % GS);
         }
     }
     __syncwarp();
