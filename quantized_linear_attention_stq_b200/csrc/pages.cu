@@ -9,7 +9,7 @@
 // plan is one block's, in one launch. A large one takes two: many blocks, each of which makes the
 // sums for itself and writes its part of the table and of the slot map, then one block that writes
 // the lengths, the starts and the list's head, which the first launch still reads when they are
-// updated in place.
+// updated in place. The second starts beside the first, makes its sums, and waits before it writes.
 //
 // Write. A row of a token's keys (all heads) is contiguous on the way in; each head's part goes to
 // its own page rows. 16-byte copies, four in flight per thread; bound by HBM.
@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(NTP) page_plan_kernel(const PlanParams p)
     __shared__ int page0[NTP];   // pages asked for by the round's requests before it
     __shared__ int taken;        // pages taken by the requests served so far
     const int tid = threadIdx.x;
+    if (!p.commit) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int head = *p.free_head;
     const bool bad_head = head < 0 || head > p.F;
     const long long avail = bad_head ? 0 : p.F - head;
@@ -121,6 +122,8 @@ __global__ void __launch_bounds__(NTP) page_plan_kernel(const PlanParams p)
         longlong2 total;
         const longlong2 upto = scan_pair(make_longlong2(add, need), warp_sums, &total);
         const long long tok = tok_base + upto.x - add, pg = page_base + upto.y - need;
+        // the sums were made while the first launch ran; what it reads is written behind its end
+        if (!p.fill) asm volatile("griddepcontrol.wait;" ::: "memory");
         if (b < p.B) {
             // its pages are on the list, and its tokens in the slot map
             const bool fits = ok && (need == 0 || pg + need <= avail) && tok + add <= p.N;
@@ -166,6 +169,7 @@ __global__ void __launch_bounds__(NTP) page_plan_kernel(const PlanParams p)
     }
     if (p.fill)
         for (long long i = tok_base + at; i < p.N; i += step) p.slot_map[i] = -1;
+    if (!p.fill) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (p.commit && tid == 0) {
         p.starts[p.B] = (int)tok_base;
         *p.head_out = bad_head ? head : head + taken;
@@ -238,8 +242,16 @@ extern "C" stq_status stq_page_plan(int32_t B, int32_t table_width, int32_t page
     if (cudaGetLastError() != cudaSuccess) return STQ_ERR_CUDA;
     p.fill = 0;
     p.commit = 1;
-    stq::page_plan_kernel<<<1, stq::NTP, 0, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? STQ_OK : STQ_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(stq::NTP);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, stq::page_plan_kernel, p) == cudaSuccess ? STQ_OK : STQ_ERR_CUDA;
 }
 
 extern "C" stq_status stq_page_write(int32_t N, int32_t kv_heads, int32_t d, int32_t dtype, int32_t page_size,
