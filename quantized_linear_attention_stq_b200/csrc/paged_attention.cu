@@ -860,7 +860,8 @@ extern "C" stq_status stq_paged_attention(int32_t B, int32_t q_heads, int32_t kv
         p.first_tile = static_cast<long long *>(workspace);
         p.pieces = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + prefix_bytes(B));
         const int64_t most = units * ((span + stq::paged::TK - 1) / stq::paged::TK);
-        grid = (dtype == STQ_BF16 ? 2 : 4) * (int64_t)sms;  // the blocks that fit at a time
+        // the blocks that fit at a time, by their registers (fp32, more than four rows) and shared memory
+        grid = (dtype == STQ_BF16 || group > 4 ? 2 : d == 128 ? 3 : 4) * (int64_t)sms;
         if (grid > stq::paged::kMaxBlocks) grid = stq::paged::kMaxBlocks;
         if (grid > most) grid = most > 0 ? most : 1;
     }
