@@ -302,6 +302,9 @@ struct Terms {
     static constexpr int PRODUCTS = GROUP == 4 ? 1 : GROUP == 8 ? 2 : 3;
 };
 
+// Blocks on an SM, by shared memory and registers.
+constexpr int mma_blocks(int d) { return d == 128 ? 2 : d == 64 ? 3 : 4; }
+
 template <int D>
 struct MmaCfg {
     static constexpr int CH = D / 8;                   // 16-byte chunks of a row
@@ -656,7 +659,7 @@ __global__ void __launch_bounds__(NTA) paged_simt_kernel(const Params p)
 }
 
 template <int D, int GROUP>
-__global__ void __launch_bounds__(NTA, 2) paged_mma_kernel(const Params p)
+__global__ void __launch_bounds__(NTA, mma_blocks(D)) paged_mma_kernel(const Params p)
 {
     extern __shared__ __align__(128) uint8_t raw[];
     float *sums = reinterpret_cast<float *>(raw + MmaCfg<D>::MAIN), *m = sums + ROWS * D, *l = m + ROWS;
@@ -672,6 +675,7 @@ constexpr int NTJ = 256;
 __global__ void __launch_bounds__(NTJ) paged_join_kernel(const Params p, int d, int most_blocks)
 {
     __shared__ float weight[kMaxBlocks], red[NTJ], lsum[NTJ];
+    __shared__ float4 sums[NTJ];
     // started while the attention kernel runs; every thread waits for its end, so that what follows
     // on the stream follows both
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -741,24 +745,40 @@ __global__ void __launch_bounds__(NTJ) paged_join_kernel(const Params p, int d, 
     }
     lsum[tid] = l;
     __syncthreads();
-    const int c = tid % d, cls = tid / d, classes = NTJ / d;
-    float sum = 0.f;
+    // four columns to a thread: sixteen bytes of eight pieces are on their way at a time
+    const int c4s = d / 4, c4 = tid % c4s, cls = tid / c4s, classes = NTJ / c4s;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-    for (int i = cls; i < n; i += classes) sum = fmaf(weight[i], piece(i)[r * d + c], sum);
-    red[tid] = sum;
+    for (int i = cls; i < n; i += classes) {
+        const float4 x = *reinterpret_cast<const float4 *>(piece(i) + r * d + 4 * c4);
+        const float w = weight[i];
+        sum = make_float4(fmaf(w, x.x, sum.x), fmaf(w, x.y, sum.y), fmaf(w, x.z, sum.z), fmaf(w, x.w, sum.w));
+    }
+    sums[tid] = sum;
     __syncthreads();
 #pragma unroll
     for (int h = NTJ / 2; h > 0; h >>= 1) {
         if (tid < h) {
             lsum[tid] += lsum[tid + h];
-            if (h >= d) red[tid] += red[tid + h];
+            if (h >= c4s) {
+                const float4 x = sums[tid + h];
+                sum = make_float4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
+                sums[tid] = sum;
+            }
         }
         __syncthreads();
     }
-    if (tid < d) {
-        const float out = lsum[0] == 0.f ? 0.f : red[tid] / lsum[0];
-        if (!(fabsf(out) <= 3.402823466e38f)) flag(p.status, kFlagNonfinite);
-        o[tid] = out;
+    if (tid < c4s) {
+        const float l = lsum[0];
+        const float out[4] = {sum.x / l, sum.y / l, sum.z / l, sum.w / l};
+        bool bad = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float x = l == 0.f ? 0.f : out[e];
+            bad |= !(fabsf(x) <= 3.402823466e38f);
+            o[4 * tid + e] = x;
+        }
+        if (bad) flag(p.status, kFlagNonfinite);
     }
 }
 
@@ -861,7 +881,7 @@ extern "C" stq_status stq_paged_attention(int32_t B, int32_t q_heads, int32_t kv
         p.pieces = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + prefix_bytes(B));
         const int64_t most = units * ((span + stq::paged::TK - 1) / stq::paged::TK);
         // the blocks that fit at a time, by their registers (fp32, more than four rows) and shared memory
-        grid = (dtype == STQ_BF16 || group > 4 ? 2 : d == 128 ? 3 : 4) * (int64_t)sms;
+        grid = (dtype == STQ_BF16 ? stq::mma_blocks(d) : group > 4 ? 2 : d == 128 ? 3 : 4) * (int64_t)sms;
         if (grid > stq::paged::kMaxBlocks) grid = stq::paged::kMaxBlocks;
         if (grid > most) grid = most > 0 ? most : 1;
     }
