@@ -187,24 +187,40 @@ struct WriteParams {
     int64_t slots;               // pages * page
 };
 
-__global__ void __launch_bounds__(256) page_write_kernel(const WriteParams p)
+constexpr int NTW = 256, PIECES = 2;  // threads; pieces of k, and of v, of a thread
+
+// A block takes NTW * PIECES pieces in a row, so that one 64-bit division serves them all.
+__global__ void __launch_bounds__(NTW) page_write_kernel(const WriteParams p)
 {
-    const int64_t step = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < p.pieces; i += step) {
-        const int64_t t = i / p.row_pieces;
-        const int c = (int)(i - t * p.row_pieces), h = c / p.head_pieces, x = c - h * p.head_pieces;
+    const int64_t base = (int64_t)blockIdx.x * (NTW * PIECES), t0 = base / p.row_pieces;
+    const unsigned rest = (unsigned)(base - t0 * p.row_pieces) + threadIdx.x;
+    uint4 a[PIECES], b[PIECES];
+    size_t dst[PIECES];
+    bool live[PIECES];
+#pragma unroll
+    for (int u = 0; u < PIECES; ++u) {
+        const unsigned j = rest + u * NTW, dt = j / (unsigned)p.row_pieces, c = j - dt * (unsigned)p.row_pieces;
+        const int64_t t = t0 + dt;
+        live[u] = base + threadIdx.x + u * NTW < p.pieces;
+        if (!live[u]) continue;
         const int slot = p.slot_map[t];
         if (slot < 0 || slot >= p.slots) {
             if (slot != -1) flag(p.status, kFlagBounds);
+            live[u] = false;
             continue;
         }
+        const unsigned h = c / (unsigned)p.head_pieces, x = c - h * (unsigned)p.head_pieces;
         const int pg = slot / p.page, off = slot - pg * p.page;
-        const size_t dst = ((((size_t)pg * p.heads + h) * p.page + off) * p.head_pieces + x) * 16;
-        const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p.k + t * p.k_stride + c * 16));
-        const uint4 b = __ldcs(reinterpret_cast<const uint4 *>(p.v + t * p.v_stride + c * 16));
-        *reinterpret_cast<uint4 *>(p.k_pages + dst) = a;
-        *reinterpret_cast<uint4 *>(p.v_pages + dst) = b;
+        dst[u] = ((((size_t)pg * p.heads + h) * p.page + off) * p.head_pieces + x) * 16;
+        a[u] = __ldcs(reinterpret_cast<const uint4 *>(p.k + t * p.k_stride + (size_t)c * 16));
+        b[u] = __ldcs(reinterpret_cast<const uint4 *>(p.v + t * p.v_stride + (size_t)c * 16));
     }
+#pragma unroll
+    for (int u = 0; u < PIECES; ++u)
+        if (live[u]) {
+            *reinterpret_cast<uint4 *>(p.k_pages + dst[u]) = a[u];
+            *reinterpret_cast<uint4 *>(p.v_pages + dst[u]) = b[u];
+        }
 }
 
 }  // namespace
@@ -285,7 +301,8 @@ extern "C" stq_status stq_page_write(int32_t N, int32_t kv_heads, int32_t d, int
     p.row_pieces = kv_heads * p.head_pieces;
     p.pieces = (int64_t)N * p.row_pieces;
     p.slots = (int64_t)num_pages * page_size;
-    const int64_t want = (p.pieces + 255) / 256;
-    stq::page_write_kernel<<<(unsigned)(want < 65536 ? want : 65536), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    const int64_t blocks = (p.pieces + stq::NTW * stq::PIECES - 1) / (stq::NTW * stq::PIECES);
+    if (blocks > 0x7fffffff) return STQ_ERR_UNSUPPORTED;
+    stq::page_write_kernel<<<(unsigned)blocks, stq::NTW, 0, static_cast<cudaStream_t>(stream)>>>(p);
     return cudaGetLastError() == cudaSuccess ? STQ_OK : STQ_ERR_CUDA;
 }
