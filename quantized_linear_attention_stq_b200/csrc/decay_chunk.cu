@@ -134,6 +134,14 @@ __device__ __forceinline__ void tmem_st_16x8(uint32_t taddr, const uint32_t (&r)
                  : "memory");
 }
 
+// The largest magnitude of three; NaN where one is.
+__device__ __forceinline__ float max_abs3(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // Eight columns of this thread's lane.
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8])
 {
@@ -383,7 +391,7 @@ __global__ void __launch_bounds__(NTC, 1)
             const uint32_t z[16] = {}, z8[8] = {};
             for (int c = top + 1 + sub; c < 8; c += 2)  // tokens behind the row's: zero in every chunk
                 tmem_st8(tl + TM_L + 8 * c, z8);
-            float bad = 0.f;  // 0 x is not 0 for an x that is not finite
+            float most = 0.f;
             for (int n = 0; n < N; ++n) {
                 const int t0 = (n0 + n) * CT;
                 if (!wait(GA, n)) break;
@@ -474,8 +482,8 @@ __global__ void __launch_bounds__(NTC, 1)
                     if (at >= d) break;
                     if (t0 + t < len)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (i < 16 || d > 16) bad = fmaf(o[cc][i], 0.f, bad);
+                        for (int i = 0; i < 32; i += 2)
+                            if (i < 16 || d > 16) most = max_abs3(most, o[cc][i], o[cc][i + 1]);
                     if (whole) {
                         if (cc > 0) {
                             if (lane == 0) tma_stores_read();
@@ -498,7 +506,7 @@ __global__ void __launch_bounds__(NTC, 1)
                 }
             }
             if (lane == 0) tma_stores_read();
-            if (!(bad == 0.f)) flag(p.status, kFlagNonfinite);
+            if (!(most <= 3.402823466e38f)) flag(p.status, kFlagNonfinite);
         }
     } else if (warp < 16) {
         regs_up<88>();
