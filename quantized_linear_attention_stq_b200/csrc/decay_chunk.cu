@@ -36,6 +36,7 @@
 #include "../../include/stq.h"
 #include "prefill_common.cuh"
 #include "stq_decay.cuh"
+#include "stream_order.cuh"
 #include "tensor_map.cuh"
 
 namespace stq {
@@ -255,6 +256,7 @@ __global__ void __launch_bounds__(NTC, 1)
     ChunkMisc<M::GS> &ms = *reinterpret_cast<ChunkMisc<M::GS> *>(sm + M::MISC);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
+    wait_for_stream();
     // (request, head), segment of the prompt
     const int64_t item = blockIdx.x;
     const int seg = (int)(item % p.segments);
@@ -781,8 +783,7 @@ cudaError_t launch(const DecayParams &p, int d, cudaStream_t s)
     if (e != cudaSuccess) return e;
     const int64_t grid = (int64_t)p.B * p.H * p.segments;
     if (grid > 0x7fffffff) return cudaErrorNotSupported;
-    kernel<<<(unsigned)grid, NTC, ChunkCfg<KB, SUMS>::SMEM, s>>>(p, d, map[0], map[1], map[2], map[3]);
-    return cudaGetLastError();
+    return launch_early(kernel, dim3((unsigned)grid), NTC, ChunkCfg<KB, SUMS>::SMEM, s, p, d, map[0], map[1], map[2], map[3]);
 }
 
 }  // namespace

@@ -18,6 +18,7 @@
 // decays, a join turns these into the states before the segments, and the main pass then runs all
 // segments at once. The first pass costs a part of the main one, so a cut has to win more than that.
 #include "../../include/stq.h"
+#include "stream_order.cuh"
 #include "stq_decay.cuh"
 
 namespace stq {
@@ -62,6 +63,7 @@ __global__ void __launch_bounds__(StepCfg<D>::NT) decay_step_kernel(const DecayP
     __shared__ float4 part[S::RG][S::C4];
     __shared__ float qs[D], ks[D];
     const int tid = threadIdx.x, c = tid % S::C4, rg = tid / S::C4;
+    wait_for_stream();
     const size_t tile = blockIdx.x;  // (request, head)
     const int b = (int)(tile / (unsigned)p.H), h = (int)(tile - (size_t)b * p.H);
     const int slot = p.slots[b];
@@ -142,6 +144,7 @@ __global__ void __launch_bounds__(SerialCfg<D, CW>::NT) decay_serial_kernel(cons
     const int tid = threadIdx.x, r = tid % S::SL, cl = tid / S::SL * CW;
     const int seg = blockIdx.x / (D / S::CB), c0 = blockIdx.x % (D / S::CB) * S::CB;
     const size_t tile = blockIdx.y + (size_t)blockIdx.z * gridDim.y;  // (request, head)
+    wait_for_stream();
     if (tile >= (size_t)p.B * p.H) return;
     const int b = (int)(tile / (unsigned)p.H), h = (int)(tile - (size_t)b * p.H);
     const int slot = p.slots[b];
@@ -291,6 +294,7 @@ __global__ void __launch_bounds__(SerialCfg<D, CW>::NT) decay_serial_kernel(cons
 constexpr int JOIN = 8;
 __global__ void __launch_bounds__(256) decay_join_kernel(const DecayParams p, const int d)
 {
+    wait_for_stream();
     const int n4 = d * d / 4, per = (n4 + 255) / 256;
     const int64_t tile = blockIdx.x / per;
     const int i = blockIdx.x % per * 256 + threadIdx.x;
@@ -325,11 +329,7 @@ template <int D>
 cudaError_t step(const DecayParams &p, int in_bf16, cudaStream_t s)
 {
     const unsigned grid = (unsigned)((size_t)p.B * p.H);
-    if (in_bf16)
-        decay_step_kernel<D, 1><<<grid, StepCfg<D>::NT, 0, s>>>(p);
-    else
-        decay_step_kernel<D, 0><<<grid, StepCfg<D>::NT, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_early(in_bf16 ? decay_step_kernel<D, 1> : decay_step_kernel<D, 0>, dim3(grid), StepCfg<D>::NT, 0, s, p);
 }
 
 template <int D, int IN_BF16, int CW>
@@ -339,11 +339,8 @@ cudaError_t serial(const DecayParams &p, bool sums, cudaStream_t s)
     const size_t tiles = (size_t)p.B * p.H;
     const unsigned gy = (unsigned)(tiles < 32768 ? tiles : 32768);
     const dim3 grid((unsigned)p.segments * (D / S::CB), gy, (unsigned)((tiles + gy - 1) / gy));
-    if (sums)
-        decay_serial_kernel<D, IN_BF16, 1, CW><<<grid, S::NT, 0, s>>>(p);
-    else
-        decay_serial_kernel<D, IN_BF16, 0, CW><<<grid, S::NT, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_early(sums ? decay_serial_kernel<D, IN_BF16, 1, CW> : decay_serial_kernel<D, IN_BF16, 0, CW>, grid, S::NT,
+                        0, s, p);
 }
 
 template <int D, int CW>
@@ -363,8 +360,7 @@ bool serial_wide(const DecayParams &p, int d)
 cudaError_t decay_join(const DecayParams &p, int d, cudaStream_t s)
 {
     const int64_t grid = (int64_t)p.B * p.H * ((d * d / 4 + 255) / 256);
-    decay_join_kernel<<<(unsigned)grid, 256, 0, s>>>(p, d);
-    return cudaGetLastError();
+    return launch_early(decay_join_kernel, dim3((unsigned)grid), 256, 0, s, p, d);
 }
 
 // How a prompt is done: by chunks or token by token, in how many segments of how many tokens.

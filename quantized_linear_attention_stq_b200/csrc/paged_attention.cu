@@ -14,6 +14,7 @@
 // whose sum is the fp32 weight, so that o keeps fp32's accuracy. fp32 caches go through fp32 FMAs.
 #include "../../include/stq.h"
 #include "stq_paged.cuh"
+#include "stream_order.cuh"
 
 namespace stq {
 namespace {
@@ -619,6 +620,7 @@ __device__ __forceinline__ void finish(const Params &p, int b, int hk, int rt, c
 template <class Unit>
 __device__ __forceinline__ void walk(const Params &p, Unit unit)
 {
+    wait_for_stream();
     const int units = p.Hkv * p.row_tiles;
     if (!p.split) {
         const int u = blockIdx.x % units, b = blockIdx.x / units;
@@ -678,7 +680,7 @@ __global__ void __launch_bounds__(NTJ) paged_join_kernel(const Params p, int d, 
     __shared__ float4 sums[NTJ];
     // started while the attention kernel runs; every thread waits for its end, so that what follows
     // on the stream follows both
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_stream();
     const int units = p.Hkv * p.row_tiles;
     const int row = blockIdx.x % p.Hq, b = blockIdx.x / p.Hq, tid = threadIdx.x;
     const int hk = row / p.group, g = row % p.group, rt = g / ROWS, r = g % ROWS;
@@ -787,8 +789,7 @@ cudaError_t launch_one(Kernel kernel, const Params &p, unsigned grid, int bytes,
 {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, NTA, bytes, s>>>(p);
-    return cudaGetLastError();
+    return launch_early(kernel, dim3(grid), NTA, bytes, s, p);
 }
 
 template <int D>
@@ -887,15 +888,7 @@ extern "C" stq_status stq_paged_attention(int32_t B, int32_t q_heads, int32_t kv
     }
     if (stq::launch_attention(p, d, dtype == STQ_BF16, (unsigned)grid, s) != cudaSuccess) return STQ_ERR_CUDA;
     if (!p.split) return STQ_OK;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)((int64_t)B * q_heads));
-    cfg.blockDim = dim3(stq::NTJ);
-    cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, stq::paged_join_kernel, p, d, (int)grid);
+    const cudaError_t e =
+        stq::launch_early(stq::paged_join_kernel, dim3((unsigned)((int64_t)B * q_heads)), stq::NTJ, 0, s, p, d, (int)grid);
     return e == cudaSuccess ? STQ_OK : STQ_ERR_CUDA;
 }

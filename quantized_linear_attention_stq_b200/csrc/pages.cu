@@ -15,6 +15,7 @@
 // its own page rows. 16-byte copies, four in flight per thread; bound by HBM.
 #include "../../include/stq.h"
 #include "stq_internal.cuh"
+#include "stream_order.cuh"
 
 namespace stq {
 namespace {
@@ -96,6 +97,7 @@ __global__ void __launch_bounds__(NTP) page_plan_kernel(const PlanParams p)
     __shared__ int page0[NTP];   // pages asked for by the round's requests before it
     __shared__ int taken;        // pages taken by the requests served so far
     const int tid = threadIdx.x;
+    if (p.fill) wait_for_stream();
     if (!p.commit) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int head = *p.free_head;
     const bool bad_head = head < 0 || head > p.F;
@@ -123,7 +125,7 @@ __global__ void __launch_bounds__(NTP) page_plan_kernel(const PlanParams p)
         const longlong2 upto = scan_pair(make_longlong2(add, need), warp_sums, &total);
         const long long tok = tok_base + upto.x - add, pg = page_base + upto.y - need;
         // the sums were made while the first launch ran; what it reads is written behind its end
-        if (!p.fill) asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (!p.fill) wait_for_stream();
         if (b < p.B) {
             // its pages are on the list, and its tokens in the slot map
             const bool fits = ok && (need == 0 || pg + need <= avail) && tok + add <= p.N;
@@ -169,7 +171,7 @@ __global__ void __launch_bounds__(NTP) page_plan_kernel(const PlanParams p)
     }
     if (p.fill)
         for (long long i = tok_base + at; i < p.N; i += step) p.slot_map[i] = -1;
-    if (!p.fill) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!p.fill) wait_for_stream();
     if (p.commit && tid == 0) {
         p.starts[p.B] = (int)tok_base;
         *p.head_out = bad_head ? head : head + taken;
@@ -192,6 +194,7 @@ constexpr int NTW = 256, PIECES = 2;  // threads; pieces of k, and of v, of a th
 // A block takes NTW * PIECES pieces in a row, so that one 64-bit division serves them all.
 __global__ void __launch_bounds__(NTW) page_write_kernel(const WriteParams p)
 {
+    wait_for_stream();
     const int64_t base = (int64_t)blockIdx.x * (NTW * PIECES), t0 = base / p.row_pieces;
     const unsigned rest = (unsigned)(base - t0 * p.row_pieces) + threadIdx.x;
     uint4 a[PIECES], b[PIECES];
@@ -249,25 +252,15 @@ extern "C" stq_status stq_page_plan(int32_t B, int32_t table_width, int32_t page
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     // the slot map's size bounds the work: one block up to kPlanOneBlock entries
     if (slot_map_size <= stq::kPlanOneBlock) {
-        stq::page_plan_kernel<<<1, stq::NTP, 0, s>>>(p);
-        return cudaGetLastError() == cudaSuccess ? STQ_OK : STQ_ERR_CUDA;
+        return stq::launch_early(stq::page_plan_kernel, dim3(1), stq::NTP, 0, s, p) == cudaSuccess ? STQ_OK : STQ_ERR_CUDA;
     }
     const int blocks = (slot_map_size + stq::NTP - 1) / stq::NTP;
     p.commit = 0;
-    stq::page_plan_kernel<<<blocks < 296 ? blocks : 296, stq::NTP, 0, s>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return STQ_ERR_CUDA;
+    if (stq::launch_early(stq::page_plan_kernel, dim3(blocks < 296 ? blocks : 296), stq::NTP, 0, s, p) != cudaSuccess)
+        return STQ_ERR_CUDA;
     p.fill = 0;
     p.commit = 1;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(1);
-    cfg.blockDim = dim3(stq::NTP);
-    cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, stq::page_plan_kernel, p) == cudaSuccess ? STQ_OK : STQ_ERR_CUDA;
+    return stq::launch_early(stq::page_plan_kernel, dim3(1), stq::NTP, 0, s, p) == cudaSuccess ? STQ_OK : STQ_ERR_CUDA;
 }
 
 extern "C" stq_status stq_page_write(int32_t N, int32_t kv_heads, int32_t d, int32_t dtype, int32_t page_size,
@@ -303,6 +296,7 @@ extern "C" stq_status stq_page_write(int32_t N, int32_t kv_heads, int32_t d, int
     p.slots = (int64_t)num_pages * page_size;
     const int64_t blocks = (p.pieces + stq::NTW * stq::PIECES - 1) / (stq::NTW * stq::PIECES);
     if (blocks > 0x7fffffff) return STQ_ERR_UNSUPPORTED;
-    stq::page_write_kernel<<<(unsigned)blocks, stq::NTW, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return cudaGetLastError() == cudaSuccess ? STQ_OK : STQ_ERR_CUDA;
+    const cudaError_t e =
+        stq::launch_early(stq::page_write_kernel, dim3((unsigned)blocks), stq::NTW, 0, static_cast<cudaStream_t>(stream), p);
+    return e == cudaSuccess ? STQ_OK : STQ_ERR_CUDA;
 }

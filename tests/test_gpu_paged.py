@@ -519,3 +519,61 @@ def test_compiled_binding_and_python_make_the_same_calls(stq):
     for x in (q, q.as_subclass(Sub)):
         with pytest.raises(stq.StqError):
             stq.paged_attention(x, pages[0], pages[1], table, lens, out[0], float("inf"), workspace=ws)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_keep_the_streams_order(stq, captured):
+    """Kernels are set up while the one before them runs: still each reads what was written just before it, by
+    a call of the library or by torch, and is done before what follows. Run without a wait between, and with
+    one behind every operation."""
+    B, Hq, H, d, page, steps = 5, 8, 2, 64, 4, 60
+    g = torch.Generator(device=DEV).manual_seed(7)
+    rnd = lambda *s: torch.randn(s, generator=g, device=DEV)  # noqa: E731
+    noise = [rnd(B, (Hq + 2 * H) * d) for _ in range(steps)]
+    gates = [torch.rand(B, H, generator=g, device=DEV) for _ in range(steps)]
+    n, W = 200, 40
+    i32 = dict(dtype=torch.int32, device=DEV)
+    ws = torch.empty(stq.paged_attention_workspace_bytes(B, Hq, d, H), dtype=torch.uint8, device=DEV)
+
+    def run(wait):
+        table, lens, head = torch.zeros(B, W, **i32), torch.zeros(B, **i32), torch.zeros(1, **i32)
+        fresh, free, starts = torch.ones(B, **i32), torch.arange(n, **i32).flip(0).contiguous(), torch.zeros(B + 1, **i32)
+        slots, smap = torch.arange(B, **i32), torch.zeros(B, **i32)
+        pages = [torch.zeros(n, H, page, d, device=DEV) for _ in range(2)]
+        states, o, o2, x = torch.zeros(B, H, d, d, device=DEV), torch.zeros(B, Hq, d, device=DEV), torch.zeros(B, H, d, device=DEV), torch.zeros(B, d, device=DEV)
+        outs = torch.zeros(steps, B, d, device=DEV)
+
+        def body():
+            for s in range(steps):
+                ops = [
+                    lambda: stq.page_plan(table, lens, fresh, free, head, smap, starts, lens, head, page),
+                    lambda: torch.add(noise[s], x.repeat(1, Hq + 2 * H), out=qkv),
+                    lambda: torch.tanh(qkv, out=qkv),
+                    lambda: stq.page_write(*pages, smap, qkv[:, Hq * d:(Hq + H) * d].view(B, H, d), qkv[:, (Hq + H) * d:].view(B, H, d)),
+                    lambda: q.copy_(qkv[:, :Hq * d].view(B, Hq, d)),
+                    lambda: stq.paged_attention(q, *pages, table, lens, o, 0.125, workspace=ws),
+                    lambda: stq.decay_step(states, slots, o[:, :H].contiguous(), o[:, H:2 * H].contiguous(), o[:, 2 * H:3 * H].contiguous(), gates[s], o2),
+                    lambda: torch.sum(o2, dim=1, out=x),
+                    lambda: outs[s].copy_(x),
+                ]
+                for op in ops:
+                    op()
+                    if wait:
+                        torch.cuda.synchronize()
+
+        qkv, q = torch.zeros(B, (Hq + 2 * H) * d, device=DEV), torch.zeros(B, Hq, d, device=DEV)
+        if captured and not wait:
+            first = [t.clone() for t in (table, lens, head, states, x, *pages)]
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                body()
+            for t, was in zip((table, lens, head, states, x, *pages), first):
+                t.copy_(was)
+            graph.replay()
+        else:
+            body()
+        torch.cuda.synchronize()
+        return outs, states, pages[0], pages[1], lens
+
+    for a, b in zip(run(False), run(True)):
+        assert torch.equal(a, b)
