@@ -126,9 +126,9 @@ template <int D, int CW>
 struct SerialCfg {
     static constexpr int SL = D >= 32 ? 8 : 4;                     // lanes sharing a column
     static constexpr int RW = D / SL;                              // rows of a thread
-    static constexpr int CB = CW == 1 ? (D < 32 ? D : 32) : (D < 64 ? D : 64);  // columns of a CTA
+    static constexpr int CB = CW == 1 ? (D == 32 ? 32 : 16) : (D < 64 ? D : 64);  // columns of a CTA
     static constexpr int NT = CB / CW * SL;
-    static constexpr int TB = D < 32 ? 32 : 16;                              // tokens staged at a time
+    static constexpr int TB = CW == 4 ? 16 : D == 32 ? 28 : D == 128 ? 16 : 32;  // tokens staged at a time
 };
 
 template <int D, int IN_BF16, int SUMS, int CW>
@@ -350,11 +350,11 @@ cudaError_t serial(const DecayParams &p, int in_bf16, bool sums, cudaStream_t s)
 }
 
 // Four columns to a thread feed the FMAs from a quarter of the shared memory's reads, one to a thread
-// makes four times the warps. 32 heads of 2048 tokens of d = 128: 284 us with four, 479 with one; 4 heads of
-// 500 tokens of d = 64: 44 and 34 us.
+// makes four times the warps. With four and with one, 77 to 100 tokens: d = 128, 32 heads 23 and 17 us, 64 heads
+// 23 and 31; d = 64, 64 heads 15 and 11, 128 heads 19 and 23; d = 32, 160 heads 15.6 and 14.5, 320 heads 19 and 21.
 bool serial_wide(const DecayParams &p, int d)
 {
-    return (int64_t)p.B * p.H * p.segments * d > 148 * 128;
+    return (int64_t)p.B * p.H * p.segments * d > 50 * 128;
 }
 
 cudaError_t decay_join(const DecayParams &p, int d, cudaStream_t s)
