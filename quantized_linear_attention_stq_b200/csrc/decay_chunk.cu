@@ -26,9 +26,9 @@
 // each waited for with a limit; a barrier's next phase needs its waiter's progress, so no wait can miss
 // its phase.
 //
-// Bound by the power limit: 16 x 16 heads of 8192 tokens of d = 128 take 653 us in 20 passes, 763 in a
+// Bound by the power limit: 16 x 16 heads of 8192 tokens of d = 128 take 650 us in 20 passes, 750 in a
 // second of them, at 1.6 GHz; their tensor work alone would take 415 and 496 us at cuBLAS's rates, their
-// bytes 415. A chunk takes 8500 cycles, 6500 of them of the tensor pipe. 16 heads of 65521 tokens, in nine
+// bytes 415. A chunk takes 8200 cycles, 6500 of them of the tensor pipe. 16 heads of 65521 tokens, in nine
 // segments: 420 us, of which the main pass takes 289, the first 104 and the join 7 (floor 206 us of bytes).
 //
 // A group of 16 scores (16 fp32 columns of Tensor Memory) is replaced in place by the h and m terms of

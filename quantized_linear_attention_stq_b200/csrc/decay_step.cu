@@ -11,7 +11,7 @@
 // Token by token (fp32 inputs, short prompts). The state of a block of columns stays in registers for the
 // whole prompt (columns of S are independent of each other); tokens are staged through shared memory 16 or
 // 32 at a time. A column's rows are spread over SL lanes, joined by shuffles per token. Bound by the FMAs,
-// three to an entry and token (32 heads of 2048 tokens of d = 128: 284 us, of which 89 at the FMAs' rate).
+// three to an entry and token (32 heads of 2048 tokens of d = 128: 269 us, of which 89 at the FMAs' rate).
 //
 // Segments. Where there are too few heads to fill the GPU, prompts are cut into segments: a first
 // pass over all but the last makes each segment's own sum (from an empty state) and the product of its
