@@ -6,10 +6,10 @@
 // P(len_b + new_b) - P(len_b) more. Two prefix sums over the requests, of new tokens and of asked
 // pages, give every request its place in the slot map and in the free list, so the result does not
 // depend on the order in which threads run. Bound by launch and memory latency, not by bytes. A small
-// plan is one block's, in one launch. A large one takes two: many blocks, each of which makes the
-// sums for itself and writes its part of the table and of the slot map, then one block that writes
-// the lengths, the starts and the list's head, which the first launch still reads when they are
-// updated in place. The second starts beside the first, makes its sums, and waits before it writes.
+// plan is one block's. A large one is that of many blocks, each of which makes the sums for itself and
+// writes its part of the table and of the slot map; the first also writes the lengths, the starts and the
+// list's head, unless these are updated in place and the other blocks still read them. Then a second
+// launch of one block writes them: it starts beside the first, makes its sums, and waits before it writes.
 //
 // Write. A row of a token's keys (all heads) is contiguous on the way in; each head's part goes to
 // its own page rows. 16-byte copies, four in flight per thread; bound by HBM.
@@ -29,7 +29,7 @@ struct PlanParams {
     int32_t *slot_map, *starts, *lens_out, *head_out, *status;
     int32_t B, W, page, F, N;
     int fill;    // this launch writes the table and the slot map
-    int commit;  // this launch (of one block) writes the lengths, the starts and the list's head
+    int commit;  // the first block of this launch writes the lengths, the starts and the list's head
 };
 
 // Inclusive prefix sums of a pair of 64-bit counts over the CTA; *total gets the CTA's sums.
@@ -99,10 +99,11 @@ __global__ void __launch_bounds__(NTP) page_plan_kernel(const PlanParams p)
     const int tid = threadIdx.x;
     if (p.fill) wait_for_stream();
     if (!p.commit) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const bool commits = p.commit && blockIdx.x == 0;
     const int head = *p.free_head;
     const bool bad_head = head < 0 || head > p.F;
     const long long avail = bad_head ? 0 : p.F - head;
-    const bool speaks = p.commit != 0;  // one launch of a call reports what it finds
+    const bool speaks = commits;  // one block of a call reports what it finds
     long long tok_base = 0, page_base = 0;
     if (tid == 0) {
         taken = 0;
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(NTP) page_plan_kernel(const PlanParams p)
             page0[tid] = (int)min(upto.y - need, 0x7fffffffLL);
             if (fits && need > 0) atomicMax(&taken, (int)(pg + need));
             if (!fits && speaks) flag(p.status, kFlagBounds);
-            if (p.commit) {
+            if (commits) {
                 p.starts[b] = token0[tid];
                 p.lens_out[b] = fits ? len + add : len;
             }
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(NTP) page_plan_kernel(const PlanParams p)
     if (p.fill)
         for (long long i = tok_base + at; i < p.N; i += step) p.slot_map[i] = -1;
     if (!p.fill) wait_for_stream();
-    if (p.commit && tid == 0) {
+    if (commits && tid == 0) {
         p.starts[p.B] = (int)tok_base;
         *p.head_out = bad_head ? head : head + taken;
     }
@@ -255,9 +256,15 @@ extern "C" stq_status stq_page_plan(int32_t B, int32_t table_width, int32_t page
         return stq::launch_early(stq::page_plan_kernel, dim3(1), stq::NTP, 0, s, p) == cudaSuccess ? STQ_OK : STQ_ERR_CUDA;
     }
     const int blocks = (slot_map_size + stq::NTP - 1) / stq::NTP;
-    p.commit = 0;
+    auto apart = [](const int32_t *x, int64_t nx, const int32_t *y, int64_t ny) { return x + nx <= y || y + ny <= x; };
+    bool in_place = !apart(head_out, 1, free_head, 1);
+    for (const int32_t *in : {lens, fresh})
+        in_place = in_place || !apart(lens_out, B, in, B) || !apart(starts, (int64_t)B + 1, in, B) || !apart(head_out, 1, in, B);
+    in_place = in_place || !apart(lens_out, B, free_head, 1) || !apart(starts, (int64_t)B + 1, free_head, 1);
+    p.commit = !in_place;
     if (stq::launch_early(stq::page_plan_kernel, dim3(blocks < 296 ? blocks : 296), stq::NTP, 0, s, p) != cudaSuccess)
         return STQ_ERR_CUDA;
+    if (!in_place) return STQ_OK;
     p.fill = 0;
     p.commit = 1;
     return stq::launch_early(stq::page_plan_kernel, dim3(1), stq::NTP, 0, s, p) == cudaSuccess ? STQ_OK : STQ_ERR_CUDA;

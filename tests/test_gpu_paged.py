@@ -577,3 +577,20 @@ def test_calls_keep_the_streams_order(stq, captured):
 
     for a, b in zip(run(False), run(True)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("lens_in_place", [False, True])
+@pytest.mark.parametrize("head_in_place", [False, True])
+def test_plan_large_map_partly_in_place(stq, lens_in_place, head_in_place):
+    """Many blocks' plan with either, both or none of the lengths and the head updated in place."""
+    table, lens, fresh, free = plan_case(200, 8, 60, 300, 5)
+    N = sum(fresh) + 7
+    assert N > 20000
+    want = run_plan(stq, table, lens, fresh, free, 0, N, 8, False)
+    t = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    for _ in range(5):
+        tt, ll, ff, fr, hh = t(table), t(lens), t(fresh), t(free), t([0])
+        lo, ho = ll if lens_in_place else t([-9] * len(lens)), hh if head_in_place else t([-9])
+        smap, starts, status = t([-7] * N), t([-7] * (len(lens) + 1)), t([0])
+        stq.page_plan(tt, ll, ff, fr, hh, smap, starts, lo, ho, 8, status=status)
+        assert (tt.tolist(), lo.tolist(), smap.tolist(), starts.tolist(), ho.item(), status.item()) == want
