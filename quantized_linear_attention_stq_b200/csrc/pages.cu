@@ -117,7 +117,8 @@ __global__ void __launch_bounds__(NTP) page_plan_kernel(const PlanParams p)
         if (b < p.B) {
             len = p.lens[b];
             add = p.fresh[b];
-            ok = len >= 0 && add >= 0 && (long long)len + add <= (long long)p.W * p.page;
+            // counts and positions are int32: a row may span more, a request may not hold more
+            ok = len >= 0 && add >= 0 && (long long)len + add <= min((long long)p.W * p.page, 0x7fffffffLL);
             add = max(add, 0);
             if (ok)
                 need = (int)(((long long)len + add + p.page - 1) / p.page - ((long long)len + p.page - 1) / p.page);

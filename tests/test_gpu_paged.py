@@ -594,3 +594,22 @@ def test_plan_large_map_partly_in_place(stq, lens_in_place, head_in_place):
         smap, starts, status = t([-7] * N), t([-7] * (len(lens) + 1)), t([0])
         stq.page_plan(tt, ll, ff, fr, hh, smap, starts, lo, ho, 8, status=status)
         assert (tt.tolist(), lo.tolist(), smap.tolist(), starts.tolist(), ho.item(), status.item()) == want
+
+
+@pytest.mark.parametrize("N", [60, 5000])  # one block's plan, and that of many
+def test_plan_refuses_lengths_past_int32(stq, N):
+    """A table row may span more than int32 counts: a request whose tokens pass it gets no slots, keeps its
+    length and is flagged; one that ends at the last count is served, and so are those behind."""
+    page, most = 1 << 30, 2147483647
+    table = [[0, 1, -1], [0, 1, -1], [0, -1, -1], [0, 1, -1]]
+    lens, fresh = [most - 7, most - 20, 5, most], [20, 20, 3, 1]
+    for inplace in (False, True):
+        got = run_plan(stq, table, lens, fresh, [2, 3], 0, N, page, inplace)
+        assert got[0] == table and got[1] == [most - 7, most, 8, most]
+        assert got[2] == [-1] * 20 + list(range(most - 20, most)) + [5, 6, 7] + [-1] * (N - 43)
+        assert got[3] == [0, 20, 40, 43, 44] and got[4] == 0 and got[5] == 1 << 6
+    # a row of many pages, and the request that is refused in front of its last page
+    table, free = [list(range(2048)) + [-1] * 2048], [7, 8]
+    got = run_plan(stq, table, [most - 99], [200], free, 0, N, 1 << 20)
+    assert got[0] == table and got[1] == [most - 99] and got[4] == 0 and got[5] == 1 << 6
+    assert got[2] == [-1] * N and got[3] == [0, min(200, N)]
