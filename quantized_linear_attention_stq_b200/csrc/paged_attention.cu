@@ -161,12 +161,13 @@ __device__ __forceinline__ void simt_unit(const Params &p, SimtSmem<D, GT> &sm, 
     const int32_t *row = p.table + (size_t)b * p.W;
     const int first = t0 * TK, last = min(len, t1 * TK), N = (last - first + KT - 1) / KT;
     auto look_up = [&](int n) {  // warp 0: the places of stage n's keys
-        const int t = first + n * KT + lane;
+        // unsigned: the look-up runs up to 94 tokens past the last, which may be close to int32's end
+        const unsigned t = (unsigned)first + (unsigned)(n * KT + lane);
         long long at = -1;
-        if (t < last) {
-            const int pg = row[t / p.page];
+        if (t < (unsigned)last) {
+            const int pg = row[t / (unsigned)p.page];
             if (pg >= 0 && pg < p.num_pages)
-                at = (((long long)pg * p.Hkv + hk) * p.page + t % p.page) * D;
+                at = (((long long)pg * p.Hkv + hk) * p.page + t % (unsigned)p.page) * D;
             else
                 flag(p.status, kFlagBounds);
         }

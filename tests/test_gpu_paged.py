@@ -613,3 +613,26 @@ def test_plan_refuses_lengths_past_int32(stq, N):
     got = run_plan(stq, table, [most - 99], [200], free, 0, N, 1 << 20)
     assert got[0] == table and got[1] == [most - 99] and got[4] == 0 and got[5] == 1 << 6
     assert got[2] == [-1] * N and got[3] == [0, min(200, N)]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_attend_up_to_the_last_position(stq, kind):
+    """A cache whose last tokens stand within a hundred of the last that a call takes (2^31 - 65). Every
+    entry of the table names the same page, so the softmax is that over the page's rows.
+
+    A block's sums are those of 2^31 / (64 * 592) tiles at least, added one after the other: with at most four
+    additions a tile and 592 pieces, n = 4 * 56680 + 592 in the bound that stands at the head of this file."""
+    page, W, d = 38820, 55319, 16
+    L = page * W
+    assert 2 ** 31 - 94 <= L <= 2 ** 31 - 65
+    g = torch.Generator(device=DEV).manual_seed(12)
+    kp, vp = (torch.randn(3, 1, page, d, generator=g, device=DEV).to(kind) for _ in range(2))
+    q = torch.randn(1, 1, d, generator=g, device=DEV).to(kind)
+    table, lens = torch.ones(1, W, dtype=torch.int32, device=DEV), torch.tensor([L], dtype=torch.int32, device=DEV)
+    o, status = torch.empty(1, 1, d, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws = torch.empty(stq.paged_attention_workspace_bytes(1, 1, d, 1), dtype=torch.uint8, device=DEV)
+    stq.paged_attention(q, kp, vp, table, lens, o, 0.25, workspace=ws, status=status)
+    assert status.item() == 0
+    want, mag, E = attend_ref(q, kp, vp, table, [page], 0.25)
+    n = 4 * 56680 + 592
+    assert torch.all((o.double() - want).abs() <= (4 * E + (2 * n + 16) * U) * mag)
