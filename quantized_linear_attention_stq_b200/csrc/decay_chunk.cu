@@ -48,13 +48,13 @@ constexpr uint32_t BOX = CT * 128;      // a [128 tokens][64 columns] bf16 box
 // Tensor Memory columns: scores, then P's h and m terms; its l terms; O; dS, then P V; slots of e K's terms
 constexpr uint32_t TM_SC = 0, TM_L = 128, TM_O = 192, TM_DS = 320, TM_KT = 448, KT_COLS = 24;
 
-// Decay products of a chunk, and inside groups of 16 tokens.
-struct ChunkGates {
+// Decay products of a chunk, and inside groups of 16 tokens; read two and four at a time in every stage.
+struct alignas(16) ChunkGates {
     float alpha[CT];
     float b[CT], e[CT];
     float upto[CT], behind[CT];  // the group's up to the token, and behind it
     float group[8];
-    double all;
+    float all;
 };
 
 // Loads of q, k, v landed; k free; v free; gates made / free; scores done; P made; O done; P V done; o read; e K's slots full / free; dS done / read; S's terms made; end.
@@ -63,7 +63,7 @@ enum { FQ, FK, FV = FK + 3, KE = FV + 3, VE = KE + 3, GA = VE + 3, GF = GA + 2, 
 template <int STAGES>
 struct ChunkMisc {
     unsigned long long bars[NBAR];
-    alignas(16) ChunkGates g[STAGES];
+    ChunkGates g[STAGES];
     uint32_t tmem;
 };
 
@@ -544,12 +544,10 @@ __global__ void __launch_bounds__(NTC, 1)
             umma::fence_proxy_async();
             arrive(SF);
         };
-        double upto = 1.0;  // the segment's decay
         if (!SUMS) put_state();
         for (int n = 0; n < N && ok; ++n) {
             if (!wait(GA + n % GS, n / GS)) break;
-            const float bc = (float)ms.g[n % GS].all;
-            upto *= ms.g[n % GS].all;
+            const float bc = ms.g[n % GS].all;
             arrive(GF + n % GS);
             if (!wait(DS + n % GS, n / GS)) break;
             umma::fence_after_sync();
@@ -578,7 +576,6 @@ __global__ void __launch_bounds__(NTC, 1)
                     for (int e = 0; e < 4; ++e) bad |= !(fabsf(S[c + e]) <= 3.402823466e38f);
                 }
             if (bad) flag(p.status, kFlagNonfinite);
-            if (SUMS && tid == 256) p.products[tile * p.segments + seg] = (float)upto;
         }
     } else if (warp < 24) {
         regs_down<40>();
@@ -703,6 +700,7 @@ __global__ void __launch_bounds__(NTC, 1)
             for (int i = 0; i < 4; ++i) next[i] = n < N && i < len - t ? alpha[t + i] : 1.f;
         };
         load(0);
+        Product upto;  // of the segment
         for (int n = 0; n < N; ++n) {
             const float a[4] = {next[0], next[1], next[2], next[3]};
             load(n + 1);
@@ -728,6 +726,7 @@ __global__ void __launch_bounds__(NTC, 1)
                 if (lane + o < 32) right *= z;
             }
             const double all = __shfl_sync(0xffffffffu, left, 31);
+            if (SUMS) upto.times(all);
             left = __shfl_up_sync(0xffffffffu, left, 4);
             right = __shfl_down_sync(0xffffffffu, right, 4);
             if (lane < 4) left = 1.0;
@@ -748,9 +747,10 @@ __global__ void __launch_bounds__(NTC, 1)
                 suf *= a[i];
             }
             if ((lane & 3) == 0) to.group[lane >> 2] = (float)group;
-            if (lane == 0) to.all = all;
+            if (lane == 0) to.all = (float)all;
             arrive(GA + n % GS);
         }
+        if (SUMS && ok && lane == 0) p.products[tile * p.segments + seg] = upto.packed();
     }
     __syncwarp();
     __syncthreads();

@@ -168,10 +168,10 @@ __global__ void __launch_bounds__(SerialCfg<D, CW>::NT) decay_serial_kernel(cons
 #pragma unroll
         for (int c = 0; c < CW; ++c) s[i][c] = SUMS ? 0.f : before[row(i) + c];
     const size_t base = tile * (size_t)p.T;
-    double upto = 1.0;
+    Product upto;
     // a block's inputs are loaded a block ahead
     constexpr int NQ = (S::TB * D / 4 + S::NT - 1) / S::NT, NV = (S::TB * S::CB / 4 + S::NT - 1) / S::NT;
-    static_assert(S::TB <= S::NT, "a thread has one decay of a block at most");
+    static_assert(S::TB <= 32 && S::NT % 32 == 0, "a block's decays are one warp's, one to a lane");
     Raw4<IN_BF16> rq[NQ], rk[NQ], rv[NV];
     float ra = 1.f;
     auto fetch = [&](int t0) {
@@ -208,6 +208,17 @@ __global__ void __launch_bounds__(SerialCfg<D, CW>::NT) decay_serial_kernel(cons
             if (i < n * S::CB) *reinterpret_cast<float4 *>(&vs[0][0] + i) = rv[x].value();
         }
         if (tid < n) as[tid] = ra;
+        if (SUMS && tid < 32) {  // the decays of a block are one warp's
+            Product x;
+            x.times(tid < n ? (double)ra : 1.0);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                x.m *= __shfl_xor_sync(0xffffffffu, x.m, o);
+                x.e += __shfl_xor_sync(0xffffffffu, x.e, o);
+            }
+            upto.times(x.m);
+            upto.e += x.e;
+        }
         if (end - t0 > S::TB) fetch(t0 + S::TB);
         __syncthreads();
 #pragma unroll(CW == 1 ? 8 : 2)
@@ -222,7 +233,6 @@ __global__ void __launch_bounds__(SerialCfg<D, CW>::NT) decay_serial_kernel(cons
             }
 #pragma unroll
             for (int c = 0; c < CW; ++c) acc[c] = 0.f;
-            if (SUMS) upto *= a;
 #pragma unroll
             for (int i = 0; i < S::RW; i += 4) {
                 const float4 k4 = *reinterpret_cast<const float4 *>(&ks[t][(i / 4 * S::SL + r) * 4]);
@@ -286,7 +296,7 @@ __global__ void __launch_bounds__(SerialCfg<D, CW>::NT) decay_serial_kernel(cons
             bad += s[i][c] - s[i][c];
         }
     if (bad != 0.f) flag(p.status, kFlagNonfinite);
-    if (SUMS && tid == 0 && c0 == 0) p.products[tile * p.segments + seg] = (float)upto;
+    if (SUMS && tid == 0 && c0 == 0) p.products[tile * p.segments + seg] = upto.packed();
 }
 
 // records[j] <- the state before segment j, for the segments that the prompt has. A thread per four
@@ -304,10 +314,10 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const DecayParams p, co
     const int n = (int)(((int64_t)len + p.seg_tokens - 1) / p.seg_tokens);
     float4 S = reinterpret_cast<const float4 *>(p.states + ((size_t)slot * p.H + h) * d * d)[i];
     float4 *rec = reinterpret_cast<float4 *>(p.records + (size_t)tile * p.segments * d * d) + i;
-    const float *prod = p.products + tile * p.segments;
+    const float2 *prod = p.products + tile * p.segments;
     for (int j0 = 0; j0 < n; j0 += JOIN) {
         float4 x[JOIN];
-        float a[JOIN];
+        float2 a[JOIN];
 #pragma unroll
         for (int j = 0; j < JOIN; ++j)
             if (j0 + j < n - 1) {  // the last segment has no sum of its own
@@ -319,8 +329,8 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const DecayParams p, co
             if (j0 + j < n) {
                 rec[(size_t)(j0 + j) * n4] = S;
                 if (j0 + j < n - 1)
-                    S = make_float4(fmaf(a[j], S.x, x[j].x), fmaf(a[j], S.y, x[j].y), fmaf(a[j], S.z, x[j].z),
-                                    fmaf(a[j], S.w, x[j].w));
+                    S = make_float4(carry(a[j], S.x, x[j].x), carry(a[j], S.y, x[j].y), carry(a[j], S.z, x[j].z),
+                                    carry(a[j], S.w, x[j].w));
             }
     }
 }
@@ -412,7 +422,7 @@ Split split(int B, int H, int T, int d, int in_bf16, bool cut)
 
 size_t split_bytes(const Split &r, int B, int H, int d)
 {
-    return r.segments > 1 ? (size_t)B * H * r.segments * ((size_t)d * d + 1) * sizeof(float) : 0;
+    return r.segments > 1 ? (size_t)B * H * r.segments * ((size_t)d * d + 2) * sizeof(float) : 0;
 }
 
 }  // namespace
@@ -523,7 +533,7 @@ extern "C" stq_status stq_decay_prefill(int32_t B, int32_t H, int32_t T, int32_t
     p.seg_tokens = cut.seg_tokens;
     if (cut.segments > 1) {
         p.records = static_cast<float *>(workspace);
-        p.products = p.records + (size_t)B * H * cut.segments * d * d;
+        p.products = reinterpret_cast<float2 *>(p.records + (size_t)B * H * cut.segments * d * d);
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     auto pass = [&](bool sums) {

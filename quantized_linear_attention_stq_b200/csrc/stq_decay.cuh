@@ -16,7 +16,7 @@ struct DecayParams {
     int32_t state_slots, B, H, T;
     // a prompt cut into segments (one: the whole prompt, records and products are null)
     float *records;   // [B][H][segments][d][d]: a segment's own sum, then the state before it
-    float *products;  // [B][H][segments]: the product of a segment's decays
+    float2 *products; // [B][H][segments]: the product of a segment's decays, as Product::packed gives it
     int32_t segments, seg_tokens;
 };
 
@@ -30,6 +30,35 @@ constexpr int kDecayChunk = 128;
 cudaError_t launch_decay_chunk(const DecayParams &p, int d, bool sums, cudaStream_t s);
 
 #ifdef __CUDACC__
+// A product of many decays, m 2^e: over thousands of tokens it may leave fp32's range, and fp64's, while
+// what it is multiplied with is zero, small or large enough for the result to stay within.
+struct Product {
+    double m = 1.0;
+    int e = 0;
+    __device__ __forceinline__ void times(double x)
+    {
+        m *= x;
+        if (m != 0.0 && isfinite(m)) {
+            int up;
+            m = frexp(m, &up);
+            e = min(max(e + up, -(1 << 30)), 1 << 30);
+        }
+    }
+    // (x, 0) for a product that a normal fp32 number x rounds (or zero, or not finite); else (m, e)
+    __device__ __forceinline__ float2 packed() const
+    {
+        const float x = (float)ldexp(m, e);
+        const bool fits = m == 0.0 || !isfinite(m) || (fabsf(x) >= 1.17549435e-38f && fabsf(x) <= 3.402823466e38f);
+        return fits ? make_float2(x, __int_as_float(0)) : make_float2((float)m, __int_as_float(e));
+    }
+};
+// product * S + x
+__device__ __forceinline__ float carry(float2 product, float S, float x)
+{
+    const int e = __float_as_int(product.y);
+    return e == 0 ? fmaf(product.x, S, x) : (float)ldexp((double)product.x * S, e) + x;
+}
+
 // Tokens of request b; -1 for a length outside [0, T].
 __device__ __forceinline__ int prompt_length(const DecayParams &p, int b)
 {

@@ -7,6 +7,8 @@ One step rounds a state entry three times, a readout adds d + 1 roundings. A chu
 is off by at most (3 T + 4 d + 300) u A and an output by as much of m; independent roundings add in
 quadrature, which bounds the 2-norm of the error by 4 sqrt(3 T + 4 d + 300) u of the magnitudes' norm.
 """
+import math
+
 import pytest
 import torch
 
@@ -368,3 +370,43 @@ def test_status_flags_name_no_wait_that_ran_out(stq):
         for _ in range(40):
             stq.decay_prefill(states, slots, q, k, v, alpha, o, workspace=ws, status=status)
     assert status.item() == 0, stq.status_flags(status)
+
+
+@pytest.mark.parametrize("kind,B,H,T,d,grow,rate", [
+    (torch.bfloat16, 1, 2, 7936, 64, 256, 1.8),     # segments of 2 chunks: 1.8^256 = 2e65
+    (torch.bfloat16, 1, 60, 13440, 16, 1920, 1.8),  # of 15 chunks: 1.8^1920 = 1e490, past fp64 as well
+    (torch.float32, 1, 600, 600, 16, 320, 1.4),     # of 320 tokens: 1.4^320 = 6e46
+])
+def test_prefill_segments_whose_decays_product_passes_fp32(stq, kind, B, H, T, d, grow, rate):
+    """Products of 128 decays are finite, a segment's is not: empty states stay empty, a state that is
+    cleared again is empty, one so small that it may grow that much does."""
+    assert stq.decay_prefill_workspace_bytes(B, H, T, d, kind) > 0
+
+    def mutate(q, k, v, alpha, states):
+        k[:, :, :grow] = 0
+        alpha[:, :, :grow] = rate
+        alpha[:, 1::2, :grow] *= -1
+        states.zero_()
+        n = math.floor(math.log10(rate) * grow)
+        if n < 70:  # S0 2^e rate^grow, some 1e10 (bf16's terms of S0 stay normal)
+            states[:, 0] = torch.randn(states.shape[0], d, d, generator=torch.Generator().manual_seed(1)) * 10.0 ** max(10 - n, -30)
+        if H > 4:
+            states[:, 4] = 1.0
+            alpha[:, 4, 0] = 0.0
+            alpha[:, 5, grow - 1] = 0.0
+
+    for ws in (True, False):
+        check(stq, B, H, T, d, kind, half=50.0, seed=51, mutate=mutate, ws=ws)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_prefill_segments_whose_decays_product_is_below_fp32(stq, kind):
+    """States that large decays bring down to where the segment's product is no normal fp32 number."""
+    def mutate(q, k, v, alpha, states):
+        k.zero_()
+        alpha.fill_(0.67)  # 0.67^256 = 3e-45
+        alpha[:, :, 256:] = 1.0
+        states.mul_(1e30)
+
+    H, T = (2, 7936) if kind == torch.bfloat16 else (600, 512)
+    check(stq, 1, H, T, 16, kind, seed=52, mutate=mutate)
