@@ -298,8 +298,8 @@ stq_status stq_decay_step(int32_t B, int32_t H, int32_t d, int32_t in_dtype, flo
                           const int32_t *slots, const void *q, const void *k, const void *v, const float *alpha,
                           float *o, int32_t *dev_status, void *stream);
 
-/* Workspace bytes stq_decay_prefill can use (0: it uses none for this shape). A shorter prompt may ask for
- * more than a longer one. */
+/* Workspace bytes stq_decay_prefill can use (0: it uses none for this shape). A shorter prompt of as many
+ * requests and heads never asks for more; fewer requests or heads may. */
 size_t stq_decay_prefill_workspace_bytes(int32_t B, int32_t H, int32_t T, int32_t d, int32_t in_dtype);
 
 /* The same recurrence over prompts: token t of request b is the decay step on (q, k, v, alpha) at t.

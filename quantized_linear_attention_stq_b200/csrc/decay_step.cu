@@ -17,6 +17,8 @@
 // pass over all but the last makes each segment's own sum (from an empty state) and the product of its
 // decays, a join turns these into the states before the segments, and the main pass then runs all
 // segments at once. The first pass costs a part of the main one, so a cut has to win more than that.
+#include <cmath>
+
 #include "../../include/stq.h"
 #include "stream_order.cuh"
 #include "stq_decay.cuh"
@@ -382,13 +384,43 @@ struct Split {
 constexpr int kSMs = 148;            // the workspace's size must not depend on the device in use
 constexpr int kMostSegments = 1024;  // the join goes along them
 
+// Whether a prompt goes by chunks. A chunk takes its time however few of its tokens there are. 512 heads of
+// bf16, chunk against token by token: d = 128 at 32 tokens 54 and 58 us, d = 64 at 64 tokens 33 and 34 us, d = 32
+// at 100 tokens 31 and 32 us; 8 heads of d = 16 at 200 tokens 13 and 28 us.
+bool by_chunks(int T, int d, int in_bf16) { return in_bf16 && ((int64_t)T * d >= 4096 || T >= 128); }
+
+// The most segments that a prompt of T tokens, or of fewer, is cut in: the workspace is sized for them, so that
+// one made for the longest prompt serves every shorter one. It never falls with T.
+int most_segments(int B, int H, int T, int d, int in_bf16)
+{
+    const int64_t tiles = (int64_t)B * H;
+    if (T < 128) return 1;
+    if (by_chunks(T, d, in_bf16)) {
+        // A cut wins by filling the rounds of CTAs better: `gain` of a round for every chunk of the prompt, against
+        // the best of no cut and one round. Each round more costs a CTA's start and end in both passes, 5.25
+        // chunks' time. Two rounds beside that cover the rounding of chunks to segments (all choices of the
+        // model below that have up to 4096 chunks are within the limit).
+        const int64_t chunks = ((int64_t)T + kDecayChunk - 1) / kDecayChunk;
+        if (chunks < 6 || tiles > 197) return 1;
+        const int whole = (int)(tiles + kSMs - 1) / kSMs, one = kSMs / (int)tiles < 64 ? kSMs / (int)tiles : 64;
+        const double gain = (one > 1 ? 1.5 / one : whole) - 1.5 * (double)tiles / kSMs;
+        const double n = (whole + floor(((gain > 0.0 ? gain * (double)chunks : 0.0) + 12.0) / 5.25)) * kSMs / (double)tiles;
+        const int64_t most = chunks < 64 ? chunks : 64;
+        return n < (double)most ? (n > 1.0 ? (int)n : 1) : (int)most;
+    }
+    const int64_t ctas = tiles * (d > 64 ? d / 64 : 1);
+    // CTAs to an SM (512 heads of 1024 tokens of d = 16: 165 us with 4, 152 with 8, 119 with 12)
+    const int64_t want = d <= 32 ? 12 : 8;
+    if (ctas > want * kSMs / 2) return 1;
+    int64_t n = want * kSMs / ctas;
+    n = n < T / 64 ? n : T / 64;
+    return (int)(n < kMostSegments ? n : kMostSegments);
+}
+
 Split split(int B, int H, int T, int d, int in_bf16, bool cut)
 {
-    // A chunk takes its time however few of its tokens there are. 512 heads of bf16, chunk against token by
-    // token: d = 128 at 32 tokens 54 and 58 us, d = 64 at 64 tokens 33 and 34 us, d = 32 at 100 tokens 31 and
-    // 32 us; 8 heads of d = 16 at 200 tokens 13 and 28 us.
-    Split r{in_bf16 && ((int64_t)T * d >= 4096 || T >= 128), 1, T};
-    const int64_t tiles = (int64_t)B * H;
+    Split r{by_chunks(T, d, in_bf16), 1, T};
+    const int64_t tiles = (int64_t)B * H, most = cut ? most_segments(B, H, T, d, in_bf16) : 1;
     if (r.chunk) {
         // One CTA to an SM: rounds of CTAs, each its chunks and 3.5 chunks' time of start and end (20 us; 5.5
         // us a chunk). The first pass takes half of the main one's time, the join 1.5 chunks' and 0.15 a
@@ -396,7 +428,7 @@ Split split(int B, int H, int T, int d, int in_bf16, bool cut)
         const int64_t chunks = ((int64_t)T + kDecayChunk - 1) / kDecayChunk, ctas = tiles;
         double best = 0.0;
         int64_t per = chunks;
-        for (int64_t n = 1; n <= (cut ? 64 : 1) && n <= chunks; ++n) {
+        for (int64_t n = 1; n <= most; ++n) {
             const int64_t c = (chunks + n - 1) / n;
             if ((chunks + c - 1) / c != n) continue;  // fewer segments of this length do
             double t = (double)((ctas * n + kSMs - 1) / kSMs) * ((double)c + 3.5);
@@ -407,22 +439,17 @@ Split split(int B, int H, int T, int d, int in_bf16, bool cut)
         r.seg_tokens = (int)(per * kDecayChunk < 0x7fffffff ? per * kDecayChunk : 0x7fffff80);
         return r;
     }
-    const int64_t ctas = tiles * (d > 64 ? d / 64 : 1);
-    // CTAs to an SM (512 heads of 1024 tokens of d = 16: 165 us with 4, 152 with 8, 119 with 12)
-    const int64_t want = d <= 32 ? 12 : 8;
-    if (!cut || T < 128 || ctas > want * kSMs / 2) return r;
-    int64_t n = want * kSMs / ctas;
-    n = n < T / 64 ? n : T / 64;
-    n = n < kMostSegments ? n : kMostSegments;
-    const int64_t per = (((int64_t)T + n - 1) / n + 31) / 32 * 32;
+    if (most == 1) return r;
+    const int64_t per = (((int64_t)T + most - 1) / most + 31) / 32 * 32;
     r.segments = (int)((T + per - 1) / per);
     r.seg_tokens = (int)per;
     return r;
 }
 
-size_t split_bytes(const Split &r, int B, int H, int d)
+// Bytes of the records and products of so many segments a prompt.
+size_t split_bytes(int segments, int B, int H, int d)
 {
-    return r.segments > 1 ? (size_t)B * H * r.segments * ((size_t)d * d + 2) * sizeof(float) : 0;
+    return segments > 1 ? (size_t)B * H * segments * ((size_t)d * d + 2) * sizeof(float) : 0;
 }
 
 }  // namespace
@@ -511,7 +538,7 @@ extern "C" size_t stq_decay_prefill_workspace_bytes(int32_t B, int32_t H, int32_
 {
     if (B < 1 || H < 1 || T < 1 || B > 2147483647 / H || (in_dtype != STQ_F32 && in_dtype != STQ_BF16)) return 0;
     if (!(d == 16 || d == 32 || d == 64 || d == 128)) return 0;
-    return stq::split_bytes(stq::split(B, H, T, d, in_dtype == STQ_BF16, true), B, H, d);
+    return stq::split_bytes(stq::most_segments(B, H, T, d, in_dtype == STQ_BF16), B, H, d);
 }
 
 extern "C" stq_status stq_decay_prefill(int32_t B, int32_t H, int32_t T, int32_t d, int32_t in_dtype, float *states,

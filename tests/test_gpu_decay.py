@@ -410,3 +410,21 @@ def test_prefill_segments_whose_decays_product_is_below_fp32(stq, kind):
 
     H, T = (2, 7936) if kind == torch.bfloat16 else (600, 512)
     check(stq, 1, H, T, 16, kind, seed=52, mutate=mutate)
+
+
+@pytest.mark.parametrize("kind,H,d,longest,lengths", [
+    (torch.bfloat16, 2, 64, 8000, (7936, 7808, 5300, 2432, 768, 640, 127)),
+    (torch.bfloat16, 60, 16, 14000, (13440, 2049, 100)),
+    (torch.float32, 3, 32, 3000, (2999, 2500, 1300, 700, 128, 5)),
+])
+def test_prefill_workspace_of_the_longest_prompt(stq, kind, H, d, longest, lengths):
+    """A server's one workspace, made for the longest prompt, serves the shorter ones."""
+    need = stq.decay_prefill_workspace_bytes(1, H, longest, d, kind)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV)
+    for i, T in enumerate(lengths):
+        q, k, v, alpha, slots, states = (x.to(DEV) for x in make(1, H, T, d, kind, seed=60 + i, half=200.0))
+        o_ref, S_ref, m, A = recurrence(q, k, v, alpha, states[slots.long()])
+        o = torch.empty(1, H, T, d, device=DEV)
+        stq.decay_prefill(states, slots, q, k, v, alpha, o, workspace=ws)
+        close(o, o_ref, m, T, d, f"o of {T} tokens")
+        close(states[slots.long()], S_ref, A, T, d, f"states behind {T} tokens")

@@ -175,3 +175,16 @@ def test_compiled_binding_leaves_the_unusual_to_python(stq):
             f(*args, None)
         with pytest.raises(TypeError):
             f()
+
+
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("H", [1, 2, 5, 16, 31, 60, 71, 90, 149, 170, 197, 300, 900])
+def test_decay_prefill_workspace_never_falls_with_the_length(stq, H, kind):
+    """One workspace, made for the longest prompt, serves every shorter one."""
+    for d in (16, 128):
+        last = 0
+        for T in [*range(1, 9000, 61), *range(9000, 90000, 1277), 1 << 20, 1 << 24, (1 << 31) - 1]:
+            need = stq.decay_prefill_workspace_bytes(1, H, T, d, kind)
+            assert need >= last, (T, d)
+            last = need
+    assert stq.decay_prefill_workspace_bytes(1, H, 127, 128, kind) == 0
