@@ -54,7 +54,7 @@ struct alignas(16) ChunkGates {
     float b[CT], e[CT];
     float upto[CT], behind[CT];  // the group's up to the token, and behind it
     float group[8];
-    float all;
+    double all;
 };
 
 // Loads of q, k, v landed; k free; v free; gates made / free; scores done; P made; O done; P V done; o read; e K's slots full / free; dS done / read; S's terms made; end.
@@ -544,11 +544,14 @@ __global__ void __launch_bounds__(NTC, 1)
             umma::fence_proxy_async();
             arrive(SF);
         };
+        Product upto;  // the segment's decay
         if (!SUMS) put_state();
         for (int n = 0; n < N && ok; ++n) {
             if (!wait(GA + n % GS, n / GS)) break;
-            const float bc = ms.g[n % GS].all;
+            const float bc = (float)ms.g[n % GS].all;
+            if (SUMS) upto.m *= ms.g[n % GS].all;
             arrive(GF + n % GS);
+            if (SUMS) upto.settle();
             if (!wait(DS + n % GS, n / GS)) break;
             umma::fence_after_sync();
 #pragma unroll
@@ -576,6 +579,7 @@ __global__ void __launch_bounds__(NTC, 1)
                     for (int e = 0; e < 4; ++e) bad |= !(fabsf(S[c + e]) <= 3.402823466e38f);
                 }
             if (bad) flag(p.status, kFlagNonfinite);
+            if (SUMS && tid == 256) p.products[tile * p.segments + seg] = upto.packed();
         }
     } else if (warp < 24) {
         regs_down<40>();
@@ -700,7 +704,6 @@ __global__ void __launch_bounds__(NTC, 1)
             for (int i = 0; i < 4; ++i) next[i] = n < N && i < len - t ? alpha[t + i] : 1.f;
         };
         load(0);
-        Product upto;  // of the segment
         for (int n = 0; n < N; ++n) {
             const float a[4] = {next[0], next[1], next[2], next[3]};
             load(n + 1);
@@ -726,7 +729,6 @@ __global__ void __launch_bounds__(NTC, 1)
                 if (lane + o < 32) right *= z;
             }
             const double all = __shfl_sync(0xffffffffu, left, 31);
-            if (SUMS) upto.times(all);
             left = __shfl_up_sync(0xffffffffu, left, 4);
             right = __shfl_down_sync(0xffffffffu, right, 4);
             if (lane < 4) left = 1.0;
@@ -747,10 +749,9 @@ __global__ void __launch_bounds__(NTC, 1)
                 suf *= a[i];
             }
             if ((lane & 3) == 0) to.group[lane >> 2] = (float)group;
-            if (lane == 0) to.all = (float)all;
+            if (lane == 0) to.all = all;
             arrive(GA + n % GS);
         }
-        if (SUMS && ok && lane == 0) p.products[tile * p.segments + seg] = upto.packed();
     }
     __syncwarp();
     __syncthreads();

@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(SerialCfg<D, CW>::NT) decay_serial_kernel(cons
     Product upto;
     // a block's inputs are loaded a block ahead
     constexpr int NQ = (S::TB * D / 4 + S::NT - 1) / S::NT, NV = (S::TB * S::CB / 4 + S::NT - 1) / S::NT;
-    static_assert(S::TB <= 32 && S::NT % 32 == 0, "a block's decays are one warp's, one to a lane");
+    static_assert(S::TB <= S::NT, "a thread has one decay of a block at most");
     Raw4<IN_BF16> rq[NQ], rk[NQ], rv[NV];
     float ra = 1.f;
     auto fetch = [&](int t0) {
@@ -210,17 +210,6 @@ __global__ void __launch_bounds__(SerialCfg<D, CW>::NT) decay_serial_kernel(cons
             if (i < n * S::CB) *reinterpret_cast<float4 *>(&vs[0][0] + i) = rv[x].value();
         }
         if (tid < n) as[tid] = ra;
-        if (SUMS && tid < 32) {  // the decays of a block are one warp's
-            Product x;
-            x.times(tid < n ? (double)ra : 1.0);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                x.m *= __shfl_xor_sync(0xffffffffu, x.m, o);
-                x.e += __shfl_xor_sync(0xffffffffu, x.e, o);
-            }
-            upto.times(x.m);
-            upto.e += x.e;
-        }
         if (end - t0 > S::TB) fetch(t0 + S::TB);
         __syncthreads();
 #pragma unroll(CW == 1 ? 8 : 2)
@@ -235,6 +224,7 @@ __global__ void __launch_bounds__(SerialCfg<D, CW>::NT) decay_serial_kernel(cons
             }
 #pragma unroll
             for (int c = 0; c < CW; ++c) acc[c] = 0.f;
+            if (SUMS) upto.m *= a;
 #pragma unroll
             for (int i = 0; i < S::RW; i += 4) {
                 const float4 k4 = *reinterpret_cast<const float4 *>(&ks[t][(i / 4 * S::SL + r) * 4]);
@@ -266,7 +256,10 @@ __global__ void __launch_bounds__(SerialCfg<D, CW>::NT) decay_serial_kernel(cons
             }
         }
         __syncthreads();
-        if constexpr (SUMS) continue;
+        if constexpr (SUMS) {
+            upto.settle();
+            continue;
+        }
         float bad = 0.f;
         for (int i = 4 * tid; i < n * S::CB; i += 4 * S::NT) {
             float4 x;
@@ -326,14 +319,28 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const DecayParams p, co
                 x[j] = rec[(size_t)(j0 + j) * n4];
                 a[j] = prod[j0 + j];
             }
+        int far = 0;
 #pragma unroll
         for (int j = 0; j < JOIN; ++j)
-            if (j0 + j < n) {
-                rec[(size_t)(j0 + j) * n4] = S;
-                if (j0 + j < n - 1)
-                    S = make_float4(carry(a[j], S.x, x[j].x), carry(a[j], S.y, x[j].y), carry(a[j], S.z, x[j].z),
-                                    carry(a[j], S.w, x[j].w));
-            }
+            if (j0 + j < n - 1) far |= __float_as_int(a[j].y);
+        if (far == 0) {  // the usual case, free of branches along the states
+#pragma unroll
+            for (int j = 0; j < JOIN; ++j)
+                if (j0 + j < n) {
+                    rec[(size_t)(j0 + j) * n4] = S;
+                    if (j0 + j < n - 1)
+                        S = make_float4(fmaf(a[j].x, S.x, x[j].x), fmaf(a[j].x, S.y, x[j].y), fmaf(a[j].x, S.z, x[j].z),
+                                        fmaf(a[j].x, S.w, x[j].w));
+                }
+            continue;
+        }
+        for (int j = j0; j < j0 + JOIN && j < n; ++j) {
+            const float4 sum = rec[(size_t)j * n4];
+            rec[(size_t)j * n4] = S;
+            if (j < n - 1)
+                S = make_float4(carry(prod[j], S.x, sum.x), carry(prod[j], S.y, sum.y), carry(prod[j], S.z, sum.z),
+                                carry(prod[j], S.w, sum.w));
+        }
     }
 }
 

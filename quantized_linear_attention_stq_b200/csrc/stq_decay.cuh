@@ -31,25 +31,32 @@ cudaError_t launch_decay_chunk(const DecayParams &p, int d, bool sums, cudaStrea
 
 #ifdef __CUDACC__
 // A product of many decays, m 2^e: over thousands of tokens it may leave fp32's range, and fp64's, while
-// what it is multiplied with is zero, small or large enough for the result to stay within.
+// what it is multiplied with is zero, small or large enough for the result to stay within. settle() is due
+// after every 128 decays at most: m stays so far from fp64's ends that a product of 128 decays, which fits
+// fp32, leaves it within (one that is below 2^-500 has left nothing of an fp32 state).
 struct Product {
     double m = 1.0;
     int e = 0;
-    __device__ __forceinline__ void times(double x)
+    __device__ __forceinline__ void settle()
     {
-        m *= x;
-        if (m != 0.0 && isfinite(m)) {
+        const unsigned field = (unsigned)__double2hiint(m) >> 20 & 0x7FFu;  // m's exponent + 1023
+        if (field - 523u > 1000u && m != 0.0 && isfinite(m)) {
             int up;
             m = frexp(m, &up);
             e = min(max(e + up, -(1 << 30)), 1 << 30);
         }
     }
-    // (x, 0) for a product that a normal fp32 number x rounds (or zero, or not finite); else (m, e)
+    // (x, 0) for a product that a normal fp32 number x rounds (or zero, or not finite); else (a, e), a e-th
+    // power of two apart
     __device__ __forceinline__ float2 packed() const
     {
-        const float x = (float)ldexp(m, e);
-        const bool fits = m == 0.0 || !isfinite(m) || (fabsf(x) >= 1.17549435e-38f && fabsf(x) <= 3.402823466e38f);
-        return fits ? make_float2(x, __int_as_float(0)) : make_float2((float)m, __int_as_float(e));
+        int up = 0;
+        const bool plain = m == 0.0 || !isfinite(m);
+        const double a = plain ? m : frexp(m, &up);
+        const int all = e + up;
+        const float x = (float)ldexp(a, all);
+        if (plain || (fabsf(x) >= 1.17549435e-38f && fabsf(x) <= 3.402823466e38f)) return make_float2(x, __int_as_float(0));
+        return make_float2((float)a, __int_as_float(all));
     }
 };
 // product * S + x
