@@ -391,6 +391,13 @@ def _workspace(workspace, need: int, dev):
     return workspace.data_ptr(), n
 
 
+def _int32(**sizes):
+    """The library's sizes are int32, to which ctypes would cut them."""
+    for name, n in sizes.items():
+        if not -2**31 <= n < 2**31:
+            raise ValueError(f"{name}: {n} is past int32")
+
+
 def _dtype(t, name: str) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -425,6 +432,7 @@ def decay_step(states, slots, q, k, v, alpha, o, status=None, stream=None):
         raise ValueError("q must be [B, H, d]")
     code, dev = _decay_args(states, slots, q, k, v, alpha, o)
     B, H, d = q.shape
+    _int32(B=B, H=H, d=d, states=states.shape[0])
     _call(lib().stq_decay_step, "stq_decay_step", dev, status, stream, B, H, d, code, states.data_ptr(),
           states.shape[0], slots.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), alpha.data_ptr(), o.data_ptr())
 
@@ -433,6 +441,7 @@ def decay_prefill_workspace_bytes(B: int, H: int, T: int, d: int, in_dtype: torc
     """Workspace bytes decay_prefill can use (0: none for this shape)."""
     if in_dtype not in _DTYPES:
         raise TypeError(f"unsupported input dtype {in_dtype}")
+    _int32(B=B, H=H, T=T, d=d)
     return lib().stq_decay_prefill_workspace_bytes(B, H, T, d, _DTYPES[in_dtype])
 
 
@@ -449,6 +458,7 @@ def decay_prefill(states, slots, q, k, v, alpha, o, lens=None, workspace=None, s
     B, H, T, d = q.shape
     if lens is not None:
         _need(lens, "lens", torch.int32, (B,), dev)
+    _int32(B=B, H=H, T=T, d=d, states=states.shape[0])
     ws, ws_bytes = _workspace(workspace, lib().stq_decay_prefill_workspace_bytes(B, H, T, d, code), dev)
     _call(lib().stq_decay_prefill, "stq_decay_prefill", dev, status, stream, B, H, T, d, code, states.data_ptr(),
           states.shape[0], slots.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), alpha.data_ptr(),
@@ -475,7 +485,9 @@ def page_plan(table, lens, fresh, free_pages, free_head, slot_map, starts, lens_
                 raise ValueError(f"{name} must be a 1-D tensor")
             n = t.shape[0]
         _need(t, name, torch.int32, (n,), dev)
-    _call(lib().stq_page_plan, "stq_page_plan", dev, status, stream, B, W, int(page_size), table.data_ptr(),
+    page_size = int(page_size)
+    _int32(table=max(B, W), page_size=page_size, free_pages=free_pages.shape[0], slot_map=slot_map.shape[0])
+    _call(lib().stq_page_plan, "stq_page_plan", dev, status, stream, B, W, page_size, table.data_ptr(),
           lens.data_ptr(), fresh.data_ptr(), free_pages.data_ptr(), free_pages.shape[0], free_head.data_ptr(),
           slot_map.data_ptr(), slot_map.shape[0], starts.data_ptr(), lens_out.data_ptr(), head_out.data_ptr())
 
@@ -502,6 +514,7 @@ def page_write(k_pages, v_pages, slot_map, k, v, status=None, stream=None):
     (N, Hkv, d), dev = k.shape, k.device
     n, _, page, _ = _pages(k_pages, v_pages, k.dtype, Hkv, d, dev)
     _need(slot_map, "slot_map", torch.int32, (N,), dev)
+    _int32(N=N, kv_heads=Hkv, d=d, page_size=page, pages=n)
     strides = []
     for name, t in (("k", k), ("v", v)):
         if not isinstance(t, torch.Tensor) or t.dtype != k.dtype or t.device != dev or t.shape != k.shape:
@@ -516,6 +529,7 @@ def page_write(k_pages, v_pages, slot_map, k, v, status=None, stream=None):
 
 def paged_attention_workspace_bytes(B: int, q_heads: int, d: int, kv_heads: int) -> int:
     """Workspace bytes of paged_attention."""
+    _int32(B=B, q_heads=q_heads, d=d, kv_heads=kv_heads)
     return lib().stq_paged_attention_workspace_bytes(B, q_heads, d, kv_heads)
 
 
@@ -538,6 +552,7 @@ def paged_attention(q, k_pages, v_pages, table, lens, o, scale: float, workspace
     _need(table, "table", torch.int32, (B, W), dev)
     _need(lens, "lens", torch.int32, (B,), dev)
     _need(o, "o", torch.float32, (B, Hq, d), dev)
+    _int32(B=B, q_heads=Hq, kv_heads=Hkv, d=d, page_size=page, pages=n, table=W)
     ws, ws_bytes = _workspace(workspace, lib().stq_paged_attention_workspace_bytes(B, Hq, d, Hkv), dev)
     _call(lib().stq_paged_attention, "stq_paged_attention", dev, status, stream, B, Hq, Hkv, d, code, page, n, W,
           q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), lens.data_ptr(), float(scale),

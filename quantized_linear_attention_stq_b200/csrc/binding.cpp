@@ -95,7 +95,7 @@ struct Args {
 bool fits(std::initializer_list<int64_t> sizes)
 {
     for (int64_t n : sizes)
-        if (n > 2147483647) return false;
+        if (n > 2147483647 || n < -2147483648LL) return false;
     return true;
 }
 
@@ -135,7 +135,7 @@ PyObject *decay_step(PyObject *, PyObject *const *args, Py_ssize_t n)
     float *o = (float *)a.data(6, c10::kFloat, {B, H, d});
     int32_t *status = a.status(7);
     void *s = a.stream(8);
-    a.ok = a.ok && fits({B, H, P});
+    a.ok = a.ok && fits({B, H, d, P});
     return finish(a, [&] {
         return stq_decay_step((int32_t)B, (int32_t)H, (int32_t)d, code, states, (int32_t)P, slots, x[0], x[1], x[2],
                               alpha, o, status, s);

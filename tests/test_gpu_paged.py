@@ -636,3 +636,16 @@ def test_attend_up_to_the_last_position(stq, kind):
     want, mag, E = attend_ref(q, kp, vp, table, [page], 0.25)
     n = 4 * 56680 + 592
     assert torch.all((o.double() - want).abs() <= (4 * E + (2 * n + 16) * U) * mag)
+
+
+@pytest.mark.parametrize("page", [(1 << 32) + 16, 16 - (1 << 32), 1 << 70, -(1 << 70)])
+def test_page_sizes_past_int32_are_refused(stq, page):
+    """By the compiled module, without a call, and then by name."""
+    from quantized_linear_attention_stq_b200 import _binding as b
+
+    i = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    args = [torch.full((1, 3), -1, dtype=torch.int32, device=DEV), i(0), i(2), i(1, 0, 2), i(0), i(5, 5, 5), i(7, 7), i(9), i(9)]
+    assert b.page_plan(*args, page, None, None) == -1
+    with pytest.raises(ValueError, match="past int32"):
+        stq.page_plan(*args, page)
+    assert args[5].tolist() == [5, 5, 5] and args[7].item() == 9

@@ -188,3 +188,33 @@ def test_decay_prefill_workspace_never_falls_with_the_length(stq, H, kind):
             assert need >= last, (T, d)
             last = need
     assert stq.decay_prefill_workspace_bytes(1, H, 127, 128, kind) == 0
+
+
+def test_sizes_past_int32_are_refused(stq):
+    """The library's sizes are int32: what passes them is named, not cut."""
+    meta = lambda *s, t=torch.int32: torch.empty(*s, dtype=t, device="meta")  # noqa: E731
+    big, f = 1 << 32, torch.float32
+    pl = dict(table=meta(2, 5), lens=meta(2), fresh=meta(2), free_pages=meta(9), free_head=meta(1), slot_map=meta(8),
+              starts=meta(3), lens_out=meta(2), head_out=meta(1), page_size=4)
+    for name, bad in (("page_size", dict(page_size=big + 16)), ("page_size", dict(page_size=16 - big)),
+                      ("free_pages", dict(free_pages=meta(big + 9))), ("slot_map", dict(slot_map=meta(1 << 31))),
+                      ("table", dict(table=meta(2, big)))):
+        with pytest.raises(ValueError, match=f"{name}.* past int32"):
+            stq.page_plan(**{**pl, **bad})
+    with pytest.raises(ValueError, match="page_size.* past int32"):
+        stq.page_write(*[meta(1, 2, big + 4, 16, t=f)] * 2, meta(3), *[meta(3, 2, 16, t=f)] * 2)
+    with pytest.raises(ValueError, match="N.* past int32"):
+        stq.page_write(*[meta(1, 2, 4, 16, t=f)] * 2, meta(big + 3), *[meta(big + 3, 2, 16, t=f)] * 2)
+    with pytest.raises(ValueError, match="table.* past int32"):
+        stq.paged_attention(meta(2, 4, 16, t=f), *[meta(3, 2, 4, 16, t=f)] * 2, meta(2, big + 1), meta(2), meta(2, 4, 16, t=f), 1.0)
+    with pytest.raises(ValueError, match="states.* past int32"):
+        stq.decay_step(meta(big + 1, 2, 16, 16, t=f), meta(1), *[meta(1, 2, 16, t=f)] * 3, meta(1, 2, t=f), meta(1, 2, 16, t=f))
+    with pytest.raises(ValueError, match="T.* past int32"):
+        stq.decay_prefill(meta(3, 1, 16, 16, t=f), meta(1), *[meta(1, 1, big + 5, 16, t=f)] * 3, meta(1, 1, big + 5, t=f),
+                          meta(1, 1, big + 5, 16, t=f))
+    for args in ((big + 1, 2, 300, 64), (1, big + 2, 300, 64), (1, 2, big + 300, 64), (1, 2, 300, big + 64)):
+        with pytest.raises(ValueError, match="past int32"):
+            stq.decay_prefill_workspace_bytes(*args, torch.float32)
+    for args in ((big + 2, 4, 64, 2), (2, big + 4, 64, 2), (2, 4, big + 64, 2), (2, 4, 64, big + 2)):
+        with pytest.raises(ValueError, match="past int32"):
+            stq.paged_attention_workspace_bytes(*args)
