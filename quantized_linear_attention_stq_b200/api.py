@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+import warnings
 from typing import Optional, Sequence
 
 import torch
@@ -343,17 +344,31 @@ def row_impact(q, k, beta, alpha, gate: int = GATE_SCALAR, stream=None) -> torch
 _native = None
 
 
+class _Ctypes:
+    """In the compiled module's place where there is none to load: every call goes through ctypes."""
+
+    decay_step = decay_prefill = page_plan = page_write = paged_attention = staticmethod(lambda *args: -1)
+
+
 def _load():
-    """The compiled module (raises if it has not been built)."""
+    """The compiled module, or _Ctypes (with a warning) where it has not been built for this torch and Python."""
     global _native
+    from . import build
+
     lib()
+    why = ""
     try:
         from . import _binding
+
+        if getattr(_binding, "built_for", "") != build.binding_key():
+            why = f"_binding.so was built for {getattr(_binding, 'built_for', 'another torch')}, this is {build.binding_key()}"
     except ImportError as e:
-        raise ImportError(f"_binding.so is missing or was built for another torch ({e}): build it with "
-                          "`python -m quantized_linear_attention_stq_b200.build`") from e
-    _native = _binding
-    return _binding
+        why = f"no _binding.so ({e})"
+    if why:
+        warnings.warn(f"{why}: calls take longer through ctypes; `python -m quantized_linear_attention_stq_b200.build` "
+                      "builds it", RuntimeWarning, stacklevel=3)
+    _native = _Ctypes if why else _binding
+    return _native
 
 
 def _done(st: int, what: str) -> bool:

@@ -12,6 +12,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -43,19 +44,44 @@ def stale() -> bool:
     return os.path.getmtime(LIB) < max(os.path.getmtime(f) for f in deps)
 
 
-def build_binding(force: bool = False, verbose: bool = False) -> str:
-    """Compile _binding.so where its source or the public header is newer."""
-    src = os.path.join(CSRC, "binding.cpp")
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, (src, HEADER))):
-        return BINDING
+def binding_key() -> str:
+    """What the compiled module is built against: it reads torch's tensors through inlined code, so one
+    built for another torch or Python must not be loaded, even where its symbols resolve."""
     import torch
 
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+
+
+def binding_stale() -> bool:
+    src = os.path.join(CSRC, "binding.cpp")
+    if not os.path.exists(BINDING) or os.path.getmtime(BINDING) < max(map(os.path.getmtime, (src, HEADER))):
+        return True
+    with open(BINDING, "rb") as f:  # the module holds its key as a string
+        return binding_key().encode() + b"\0" not in f.read()
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """Compile _binding.so where its source or the public header is newer, or it was built against another torch
+    or Python. Returns "" (and warns) where there is no torch, host compiler or Python header to build with: the
+    calls then go through ctypes."""
+    try:
+        import torch
+    except ImportError:
+        torch = None
+    cxx, python_h = shutil.which("g++"), os.path.join(sysconfig.get_paths()["include"], "Python.h")
+    missing = "torch" if torch is None else "g++" if cxx is None else "" if os.path.exists(python_h) else python_h
+    if missing:
+        warnings.warn(f"_binding.so is not built: {missing} is missing")
+        return ""
+    if not force and not binding_stale():
+        return BINDING
+    src, key = os.path.join(CSRC, "binding.cpp"), binding_key()
     root = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
     includes = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"), cuda,
-                sysconfig.get_paths()["include"]]
+                os.path.dirname(python_h)]
     tmp = BINDING + f".tmp{os.getpid()}"
-    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f'-DSTQ_BUILT_FOR="{key}"',
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-isystem{i}" for i in includes], "-o",
            tmp, src, "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-L" + PKG,
            "-l:libstq.so", "-Wl,-rpath,$ORIGIN"]

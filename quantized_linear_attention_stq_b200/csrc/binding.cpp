@@ -268,4 +268,16 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+#ifndef STQ_BUILT_FOR
+#error "STQ_BUILT_FOR names the torch and Python that this is built against"
+#endif
+
+PyMODINIT_FUNC PyInit__binding()
+{
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", STQ_BUILT_FOR) != 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

@@ -218,3 +218,54 @@ def test_sizes_past_int32_are_refused(stq):
     for args in ((big + 2, 4, 64, 2), (2, big + 4, 64, 2), (2, 4, big + 64, 2), (2, 4, 64, big + 2)):
         with pytest.raises(ValueError, match="past int32"):
             stq.paged_attention_workspace_bytes(*args)
+
+
+def test_binding_of_another_torch_is_rebuilt_and_not_used(stq, monkeypatch):
+    """The compiled module reads torch's tensors inline: one built against another torch or Python is stale for the
+    build, and the calls go through ctypes instead of it; so they do where there is none."""
+    import sys
+
+    from quantized_linear_attention_stq_b200 import _binding, api, build
+
+    assert _binding.built_for == build.binding_key() and torch.__version__ in _binding.built_for
+    assert not build.binding_stale()
+    f, i = torch.float32, torch.int32
+    good = [torch.zeros(3, 2, 16, 16), torch.zeros(1, dtype=i), *[torch.zeros(1, 2, 16)] * 3, torch.zeros(1, 2), torch.zeros(1, 2, 16)]
+    calls = []
+    for name in ("decay_step", "decay_prefill", "page_plan", "page_write", "paged_attention"):
+        assert getattr(api._Ctypes, name)(*good) == -1
+
+    def load():
+        monkeypatch.setattr(api, "_native", None)
+        with pytest.warns(RuntimeWarning, match="ctypes"):
+            with pytest.raises(ValueError, match="expected a CUDA device"):  # the Python path's answer to CPU tensors
+                stq.decay_step(*good)
+        calls.append(api._native)
+
+    with monkeypatch.context() as m:
+        m.setattr(build, "binding_key", lambda: "torch 1.0, cpython-27")
+        assert build.binding_stale()
+        load()
+    with monkeypatch.context() as m:
+        m.setitem(sys.modules, "quantized_linear_attention_stq_b200._binding", None)
+        m.delattr(sys.modules["quantized_linear_attention_stq_b200"], "_binding")
+        load()
+    assert calls == [api._Ctypes] * 2
+    monkeypatch.setattr(api, "_native", None)
+    assert api._load() is _binding
+
+
+@pytest.mark.parametrize("what", ["g++", "Python.h"])
+def test_library_is_built_without_the_bindings_tools(stq, monkeypatch, what):
+    """Where the compiled module cannot be built the C library still is."""
+    from quantized_linear_attention_stq_b200 import build
+
+    if what == "g++":
+        which = build.shutil.which
+        monkeypatch.setattr(build.shutil, "which", lambda name: None if name == "g++" else which(name))
+    else:
+        monkeypatch.setattr(build.sysconfig, "get_paths", lambda: {"include": "/nowhere"})
+    with pytest.warns(UserWarning, match="not built"):
+        assert build.build() == build.LIB
+    with pytest.warns(UserWarning, match="not built"):
+        assert build.build_binding(force=True) == ""
