@@ -97,6 +97,9 @@ __global__ void __launch_bounds__(NTP) page_plan_kernel(const PlanParams p)
     __shared__ int page0[NTP];   // pages asked for by the round's requests before it
     __shared__ int taken;        // pages taken by the requests served so far
     const int tid = threadIdx.x;
+    // A launch that writes the table waits for all that was before the call. Of two launches, the first lets the
+    // second start only behind that wait, and writes none of the lengths, counts and list head that the second
+    // then reads at once; the status word that it may flag before its own wait is only ever OR-ed into.
     if (p.fill) wait_for_stream();
     if (!p.commit) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const bool commits = p.commit && blockIdx.x == 0;

@@ -428,3 +428,63 @@ def test_prefill_workspace_of_the_longest_prompt(stq, kind, H, d, longest, lengt
         stq.decay_prefill(states, slots, q, k, v, alpha, o, workspace=ws)
         close(o, o_ref, m, T, d, f"o of {T} tokens")
         close(states[slots.long()], S_ref, A, T, d, f"states behind {T} tokens")
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("kind,T", [(torch.bfloat16, 2000), (torch.float32, 700), (torch.bfloat16, 20)])
+def test_prompts_keep_the_streams_order(stq, kind, T, captured):
+    """Prompts (in segments, where they are long), each right behind kernels that write its inputs and lengths,
+    one of them a call of the library, and in front of ones that read its outputs: without a wait between, and
+    with one behind every operation."""
+    B, H, d, steps = 2, 2, 64, 6
+    g = torch.Generator(device=DEV).manual_seed(9)
+    noise = [0.2 * torch.randn(B, H, T, d, generator=g, device=DEV) for _ in range(steps)]
+    need = stq.decay_prefill_workspace_bytes(B, H, T, d, kind)
+    assert (need > 0) == (T > 100)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV) if need else None
+    states, slots = torch.zeros(B, H, d, d, device=DEV), torch.arange(B, dtype=torch.int32, device=DEV)
+    x, o, one = (torch.zeros(B, H, n, d, device=DEV) for n in (T, T, 1))
+    gates, lens = torch.zeros(B, H, T, device=DEV), torch.zeros(B, dtype=torch.int32, device=DEV)
+    kept, status = torch.zeros(steps, B, H, T, d, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    q, k = (torch.zeros(B, H, T, d, dtype=kind, device=DEV) for _ in range(2))
+
+    def body(do):
+        for s in range(steps):
+            do(lambda: torch.tanh(noise[s] + one, out=x))
+            do(lambda: q.copy_(x))
+            do(lambda: k.copy_(x.flip(3) * 0.1))
+            do(lambda: gates.copy_(torch.sigmoid(x[..., 0] + 3)))
+            do(lambda: lens.copy_((one[:, 0, 0, 0].abs() * 5000).int().clamp(max=9).neg() + T))
+            do(lambda: stq.decay_prefill(states, slots, q, k, q, gates, o, lens=lens, workspace=ws, status=status))
+            do(lambda: stq.decay_step(states, slots, *(t[:, :, 0].contiguous() for t in (q, k, q)), gates[:, :, 0].contiguous(),
+                                      one.view(B, H, d), status=status))
+            do(lambda: stq.decay_prefill(states, slots, q, k, q, gates, o, lens=lens, workspace=ws, status=status))
+            do(lambda: kept[s].copy_(o))
+
+    tensors = [states, x, o, one, gates, lens, kept, q, k, status]
+    first = [t.clone() for t in tensors]
+
+    def start():
+        for t, was in zip(tensors, first):
+            t.copy_(was)
+        torch.cuda.synchronize()
+
+    def waited(op):
+        op()
+        torch.cuda.synchronize()
+
+    body(waited)
+    want = [t.clone() for t in tensors]
+    start()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            body(lambda op: op())
+        start()
+        graph.replay()
+    else:
+        body(lambda op: op())
+    torch.cuda.synchronize()
+    assert status.item() == 0 and lens.min() < T  # the lengths hang on the outputs before
+    for got, w in zip(tensors, want):
+        assert torch.equal(got, w)

@@ -649,3 +649,66 @@ def test_page_sizes_past_int32_are_refused(stq, page):
     with pytest.raises(ValueError, match="past int32"):
         stq.page_plan(*args, page)
     assert args[5].tolist() == [5, 5, 5] and args[7].item() == 9
+
+
+def in_order(body, tensors, captured):
+    """What body(op) leaves in `tensors` where its operations run without a wait between, directly or captured,
+    and where each is waited for."""
+    first = [t.clone() for t in tensors]
+
+    def start():
+        for t, was in zip(tensors, first):
+            t.copy_(was)
+        torch.cuda.synchronize()
+
+    def waited(op):
+        op()
+        torch.cuda.synchronize()
+
+    start()
+    body(waited)
+    want = [t.clone() for t in tensors]
+    start()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            body(lambda op: op())
+        start()
+        graph.replay()
+    else:
+        body(lambda op: op())
+    torch.cuda.synchronize()
+    return zip(tensors, want)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("B", [200, 1100])  # one round of requests, and two
+def test_large_plans_in_place_keep_the_streams_order(stq, B, captured):
+    """Plans of many blocks that update the lengths and the list's head in place, each right behind kernels
+    that write both, and the counts, and in front of ones that read what it wrote."""
+    page, W, steps, most = 8, 30, 12, 44
+    g = torch.Generator(device=DEV).manual_seed(8)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    N = B * most // 2
+    assert N > 4096
+    a = torch.randn(2048, 2048, generator=g, device=DEV)
+    counts = torch.randint(0, most, (steps, B), generator=g, device=DEV).to(torch.int32)
+    held = torch.randint(0, 100, (steps, B), generator=g, device=DEV).to(torch.int32)
+    table, free = torch.arange(B * W, **i32).view(B, W).contiguous(), torch.arange(B * W, **i32).flip(0).contiguous()
+    lens, fresh, head, starts, smap = (torch.zeros(n, **i32) for n in (B, B, 1, B + 1, N))
+    slow, status = torch.zeros(2048, 2048, device=DEV), torch.zeros(1, **i32)
+    kept = [torch.zeros(steps, n, **i32) for n in (B, 1, B + 1, N)]
+
+    def body(do):
+        for s in range(steps):
+            do(lambda: torch.mm(a, a, out=slow))  # the writes below stand behind a slow kernel
+            do(lambda: fresh.copy_(counts[s]))
+            do(lambda: torch.add(held[s], lens % 7, out=lens))
+            do(lambda: head.copy_(slow[:1, 0].abs().clamp(max=0).int() + s))
+            do(lambda: stq.page_plan(table, lens, fresh, free, head, smap, starts, lens, head, page, status=status))
+            for to, x in zip(kept, (lens, head, starts, smap)):
+                do(lambda: to[s].copy_(x))
+
+    for got, want in in_order(body, [table, lens, head, starts, smap, status, *kept], captured):
+        assert torch.equal(got, want)
+    assert status.item() == 1 << 6  # the map ends inside some plans
