@@ -712,3 +712,28 @@ def test_large_plans_in_place_keep_the_streams_order(stq, B, captured):
     for got, want in in_order(body, [table, lens, head, starts, smap, status, *kept], captured):
         assert torch.equal(got, want)
     assert status.item() == 1 << 6  # the map ends inside some plans
+
+
+@pytest.mark.parametrize("B,new", [(2500, 20), (1025, 100)])
+def test_plan_large_map_of_more_requests_than_threads(stq, B, new):
+    """Many blocks' plans that take more than one round of requests, in place and not: all served, and with a
+    free list, a slot map or both that end inside the second round."""
+    page = 8
+    table, lens, fresh, free = plan_case(B, page, 40, new, B)
+    need = [-(-(a + b) // page) + -a // page for a, b in zip(lens, fresh)]
+    N, pages, tokens = sum(fresh), sum(need), sum(fresh[:1024])
+    assert N > 4096 and B > 1024 and tokens < N
+    check_plan(stq, table, lens, fresh, free, 0, N + 9, page)
+    check_plan(stq, table, lens, fresh, [99999] * 2 + free, 2, N, page)
+    inside = sum(need[:1024]) + max(1, (pages - sum(need[:1024])) // 2)
+    check_plan(stq, table, lens, fresh, free[:inside], 0, N, page)
+    check_plan(stq, table, lens, fresh, free, 0, tokens + (N - tokens) // 2, page)
+    check_plan(stq, table, lens, fresh, free[:inside], 0, tokens + (N - tokens) // 2 + 1, page)
+    check_plan(stq, table, lens, fresh, free[: sum(need[:1000])], 0, sum(fresh[:1010]), page)  # and inside the first
+    # requests that are refused in the first round, and others that need nothing
+    bad = list(lens)
+    bad[5], bad[1000] = -1, page * len(table[0]) + 1
+    none = [0 if i % 3 else n for i, n in enumerate(fresh)]
+    if sum(none) > 4096:
+        check_plan(stq, table, bad, none, free, 0, sum(none), page)
+    check_plan(stq, table, bad, fresh, free, 0, N, page)
