@@ -398,6 +398,8 @@ def _workspace(workspace, need: int, dev):
     """(pointer, bytes) of a workspace argument; a call that needs none ignores what it is given."""
     if workspace is None or not need:
         return None, 0
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
     if workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {dev}")
     n = workspace.numel() * workspace.element_size()

@@ -737,3 +737,71 @@ def test_plan_large_map_of_more_requests_than_threads(stq, B, new):
     if sum(none) > 4096:
         check_plan(stq, table, bad, none, free, 0, sum(none), page)
     check_plan(stq, table, bad, fresh, free, 0, N, page)
+
+
+def binding_calls(kind):
+    """For each call of the binding: its name, valid arguments in order, and which of them may have another
+    length than the others ask for."""
+    g = torch.Generator(device=DEV).manual_seed(4)
+    rnd = lambda *s: torch.randn(s, generator=g, device=DEV)  # noqa: E731
+    i = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    B, H, T, d = 2, 3, 5, 32
+    pages = lambda: rnd(6, H, 4, d).to(kind)  # noqa: E731
+    word = lambda: torch.zeros(1, dtype=torch.int32, device=DEV)  # noqa: E731
+    return {
+        "decay_step": (dict(states=rnd(4, H, d, d), slots=i(1, 3), q=rnd(B, H, d).to(kind), k=rnd(B, H, d).to(kind),
+                            v=rnd(B, H, d).to(kind), alpha=torch.rand(B, H, device=DEV), o=rnd(B, H, d), status=word()), {"states"}),
+        "decay_prefill": (dict(states=rnd(4, H, d, d), slots=i(1, 3), q=rnd(B, H, T, d).to(kind), k=rnd(B, H, T, d).to(kind),
+                               v=rnd(B, H, T, d).to(kind), alpha=torch.rand(B, H, T, device=DEV), o=rnd(B, H, T, d), lens=i(5, 2),
+                               workspace=None, status=word()), {"states"}),
+        "page_plan": (dict(table=i(0, -1, -1, 1, -1, -1).view(2, 3), lens=i(3, 1), fresh=i(2, 1), free_pages=i(4, 2, 5),
+                           free_head=i(0), slot_map=i(0, 0, 0), starts=i(0, 0, 0), lens_out=i(0, 0), head_out=i(0),
+                           page_size=4, status=word()), {"free_pages", "slot_map"}),
+        "page_write": (dict(k_pages=pages(), v_pages=pages(), slot_map=i(5, -1, 9), k=rnd(3, H, d).to(kind),
+                            v=rnd(3, H, d).to(kind), status=word()), set()),
+        "paged_attention": (dict(q=rnd(B, 2 * H, d).to(kind), k_pages=pages(), v_pages=pages(), table=i(0, 1, 5, 2).view(2, 2),
+                                 lens=i(7, 5), o=rnd(B, 2 * H, d), scale=0.2,
+                                 workspace=torch.empty(1 << 22, dtype=torch.uint8, device=DEV), status=word()), set()),
+    }
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("name", ["decay_step", "decay_prefill", "page_plan", "page_write", "paged_attention"])
+def test_compiled_binding_checks_every_argument(stq, name, kind):
+    """From valid CUDA arguments, one is replaced at a time: the compiled module makes no call, and the Python
+    one names what is wrong. What is tried is never smaller than what it stands for."""
+    from quantized_linear_attention_stq_b200 import _binding as b
+
+    args, free = binding_calls(kind)[name]
+    compiled = lambda a: getattr(b, name)(*a.values(), None)  # noqa: E731
+    assert compiled(args) == 0 and args["status"].item() == 0
+    getattr(stq, name)(**args)
+    torch.cuda.synchronize()
+    tried = 0
+    for what, t in args.items():
+        if not isinstance(t, torch.Tensor):
+            wrong = [("kind", "x")] if t is not None else []
+        else:
+            wrong = [("kind", "x"), ("cpu", t.cpu())]
+            if what != "workspace":  # that one is bytes of any shape and type
+                wrong += [("dtype", t.to(torch.float64 if t.is_floating_point() else torch.int64)), ("dims", t[None]),
+                          ("type of another kind", t.int() if t.dtype == torch.float32 else t.float())]
+                if what not in free and not (name == "paged_attention" and what == "q"):
+                    wrong += [("length", torch.cat([t, t]))]
+                wrong += [("width", torch.cat([t, t], -1))] if t.dim() > 1 and what != "table" else []
+            else:
+                wrong += [("length", t[:1024])]
+            if what in ("k", "v") and name == "page_write":  # tokens may be strided, heads may not
+                wrong += [("strides", torch.cat([t, t], 1)[:, ::2])]
+            elif t.numel() > 1:
+                wrong += [("strides", torch.stack([t, t], -1)[..., 0])]
+            if what not in ("status", "workspace", "lens"):
+                wrong += [("none", None)]
+        for how, x in wrong:
+            tried += 1
+            assert compiled({**args, what: x}) == -1, f"{what}: {how}"
+            with pytest.raises((TypeError, ValueError)):
+                getattr(stq, name)(**{**args, what: x})
+    assert tried > 25
+    torch.cuda.synchronize()
+    assert args["status"].item() == 0

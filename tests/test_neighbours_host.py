@@ -269,3 +269,12 @@ def test_library_is_built_without_the_bindings_tools(stq, monkeypatch, what):
         assert build.build() == build.LIB
     with pytest.warns(UserWarning, match="not built"):
         assert build.build_binding(force=True) == ""
+
+
+def test_workspace_of_another_kind_is_named(stq):
+    z = lambda *s, t=torch.float32: torch.zeros(*s, dtype=t)  # noqa: E731
+    i = torch.int32
+    with pytest.raises(TypeError, match="workspace"):
+        stq.paged_attention(z(2, 4, 16), z(3, 2, 8, 16), z(3, 2, 8, 16), z(2, 5, t=i), z(2, t=i), z(2, 4, 16), 1.0, workspace="x")
+    with pytest.raises(TypeError, match="workspace"):
+        stq.decay_prefill(z(1, 1, 16, 16), z(1, t=i), *[z(1, 1, 2000, 16)] * 3, z(1, 1, 2000), z(1, 1, 2000, 16), workspace=b"x")
