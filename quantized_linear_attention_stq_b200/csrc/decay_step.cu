@@ -391,34 +391,57 @@ struct Split {
 constexpr int kSMs = 148;            // the workspace's size must not depend on the device in use
 constexpr int kMostSegments = 1024;  // the join goes along them
 
-// Whether a prompt goes by chunks. A chunk takes its time however few of its tokens there are. 512 heads of
-// bf16, chunk against token by token: d = 128 at 32 tokens 54 and 58 us, d = 64 at 64 tokens 33 and 34 us, d = 32
-// at 100 tokens 31 and 32 us; 8 heads of d = 16 at 200 tokens 13 and 28 us.
-bool by_chunks(int T, int d, int in_bf16) { return in_bf16 && ((int64_t)T * d >= 4096 || T >= 128); }
-
-// The most segments that a prompt of T tokens, or of fewer, is cut in: the workspace is sized for them, so that
-// one made for the longest prompt serves every shorter one. It never falls with T.
-int most_segments(int B, int H, int T, int d, int in_bf16)
+// Whether a prompt goes by chunks, given its heads (over all requests) and whether it may be cut into segments. A
+// chunk takes its time however few of its tokens there are, and a round of heads over the SMs takes it whole;
+// token by token the time goes with the tokens, and with the heads only where they are many. Measured, us token by
+// token / by chunks:
+//   d = 128, from 32 tokens on: 128 heads 18.9 / 13.1, 512 heads 52 / 49 (32 tokens). Where heads are few the
+//     latency of a token is all there is: 1 to 16 heads 10 / 13 (64 tokens), 14.0 / 13.1 (96); 32 heads 11.5 / 13.0
+//     (48), 14.4 / 13.0 (64).
+//   d = 64, from 64 on: 1 head 6.8 / 7.6, 64 heads 8.8 / 8.1, 512 heads 30.0 / 30.2.
+//   d = 32, from 80 on: 1 head 8.6 / 6.9, 148 heads 8.8 / 8.2, 256 heads 16.1 / 14.9 (96); 512 heads 24.9 / 28.3
+//     (127), 41 / 39 (192); 1024 heads 34.6 / 49.7 (128), 66 / 70 (256), 98 / 94 (384).
+//   d = 16: an entry's share of a chunk is four times that of d = 64, so token by token, 1024 heads 115 / 190 (1024
+//     tokens), 110 heads 150 / 194 (8192), 16 heads 182 / 266 (65536); but 1 to 148 heads 9.1 / 6.7 (128) and
+//     9.8 / 9.4 (256), and 1 head 50 / 36 (32768), 91 / 49 (65536). Without a cut a token takes 0.05 us, a chunk 2.7,
+//     with up to two rounds of heads; 512 heads 85 / 106 (1024).
+bool by_chunks(int64_t tiles, int T, int d, int in_bf16, bool cut)
 {
-    const int64_t tiles = (int64_t)B * H;
-    if (T < 128) return 1;
-    if (by_chunks(T, d, in_bf16)) {
-        // A cut wins by filling the rounds of CTAs better: `gain` of a round for every chunk of the prompt, against
-        // the best of no cut and one round. Each round more costs a CTA's start and end in both passes, 5.25
-        // chunks' time. Two rounds beside that cover the rounding of chunks to segments (all choices of the
-        // model below that have up to 4096 chunks are within the limit).
-        const int64_t chunks = ((int64_t)T + kDecayChunk - 1) / kDecayChunk;
-        if (chunks < 6 || tiles > 197) return 1;
-        const int whole = (int)(tiles + kSMs - 1) / kSMs, one = kSMs / (int)tiles < 64 ? kSMs / (int)tiles : 64;
-        const double gain = (one > 1 ? 1.5 / one : whole) - 1.5 * (double)tiles / kSMs;
-        const double n = (whole + floor(((gain > 0.0 ? gain * (double)chunks : 0.0) + 12.0) / 5.25)) * kSMs / (double)tiles;
-        const int64_t most = chunks < 64 ? chunks : 64;
-        return n < (double)most ? (n > 1.0 ? (int)n : 1) : (int)most;
+    if (!in_bf16) return false;
+    switch (d) {
+        case 16:
+            if (!cut) return T >= 128 && tiles <= 2 * kSMs;
+            return (T >= 128 && T <= 256 && tiles <= kSMs) || (T >= 24576 && tiles <= 2);
+        case 32: return T >= (tiles <= 256 ? 80 : tiles <= 512 ? 128 : 256);
+        case 64: return T >= 64;
+        default: return T >= (tiles < 24 ? 88 : tiles < 48 ? 56 : 32);
     }
+}
+
+// The most segments that a prompt of T tokens, or of fewer, is cut in by chunks and token by token. Neither falls
+// with T: the workspace is sized for both, so that one made for the longest prompt serves every shorter one.
+int most_chunk_segments(int64_t tiles, int T, int in_bf16)
+{
+    // A cut wins by filling the rounds of CTAs better: `gain` of a round for every chunk of the prompt, against
+    // the best of no cut and one round. Each round more costs a CTA's start and end in both passes, 5.25
+    // chunks' time. Two rounds beside that cover the rounding of chunks to segments (all choices of the
+    // model below that have up to 4096 chunks are within the limit).
+    const int64_t chunks = ((int64_t)T + kDecayChunk - 1) / kDecayChunk;
+    if (!in_bf16 || chunks < 6 || tiles > 197) return 1;
+    const int whole = (int)(tiles + kSMs - 1) / kSMs, one = kSMs / (int)tiles < 64 ? kSMs / (int)tiles : 64;
+    const double gain = (one > 1 ? 1.5 / one : whole) - 1.5 * (double)tiles / kSMs;
+    const double n = (whole + floor(((gain > 0.0 ? gain * (double)chunks : 0.0) + 12.0) / 5.25)) * kSMs / (double)tiles;
+    const int64_t most = chunks < 64 ? chunks : 64;
+    return n < (double)most ? (n > 1.0 ? (int)n : 1) : (int)most;
+}
+
+int most_serial_segments(int64_t tiles, int T, int d, int in_bf16)
+{
     const int64_t ctas = tiles * (d > 64 ? d / 64 : 1);
     // CTAs to an SM (512 heads of 1024 tokens of d = 16: 165 us with 4, 152 with 8, 119 with 12)
     const int64_t want = d <= 32 ? 12 : 8;
-    if (ctas > want * kSMs / 2) return 1;
+    // bf16 prompts of d > 16 that go token by token are too short for a cut
+    if (T < 128 || ctas > want * kSMs / 2 || (in_bf16 && d > 16)) return 1;
     int64_t n = want * kSMs / ctas;
     n = n < T / 64 ? n : T / 64;
     return (int)(n < kMostSegments ? n : kMostSegments);
@@ -426,8 +449,9 @@ int most_segments(int B, int H, int T, int d, int in_bf16)
 
 Split split(int B, int H, int T, int d, int in_bf16, bool cut)
 {
-    Split r{by_chunks(T, d, in_bf16), 1, T};
-    const int64_t tiles = (int64_t)B * H, most = cut ? most_segments(B, H, T, d, in_bf16) : 1;
+    const int64_t tiles = (int64_t)B * H;
+    Split r{by_chunks(tiles, T, d, in_bf16, cut), 1, T};
+    const int64_t most = !cut ? 1 : r.chunk ? most_chunk_segments(tiles, T, in_bf16) : most_serial_segments(tiles, T, d, in_bf16);
     if (r.chunk) {
         // One CTA to an SM: rounds of CTAs, each its chunks and 3.5 chunks' time of start and end (20 us; 5.5
         // us a chunk). The first pass takes half of the main one's time, the join 1.5 chunks' and 0.15 a
@@ -545,7 +569,9 @@ extern "C" size_t stq_decay_prefill_workspace_bytes(int32_t B, int32_t H, int32_
 {
     if (B < 1 || H < 1 || T < 1 || B > 2147483647 / H || (in_dtype != STQ_F32 && in_dtype != STQ_BF16)) return 0;
     if (!(d == 16 || d == 32 || d == 64 || d == 128)) return 0;
-    return stq::split_bytes(stq::most_segments(B, H, T, d, in_dtype == STQ_BF16), B, H, d);
+    const int bf = in_dtype == STQ_BF16, c = stq::most_chunk_segments((int64_t)B * H, T, bf);
+    const int s = stq::most_serial_segments((int64_t)B * H, T, d, bf);
+    return stq::split_bytes(c > s ? c : s, B, H, d);
 }
 
 extern "C" stq_status stq_decay_prefill(int32_t B, int32_t H, int32_t T, int32_t d, int32_t in_dtype, float *states,

@@ -374,7 +374,8 @@ def test_status_flags_name_no_wait_that_ran_out(stq):
 
 @pytest.mark.parametrize("kind,B,H,T,d,grow,rate", [
     (torch.bfloat16, 1, 2, 7936, 64, 256, 1.8),     # segments of 2 chunks: 1.8^256 = 2e65
-    (torch.bfloat16, 1, 60, 13440, 16, 1920, 1.8),  # of 15 chunks: 1.8^1920 = 1e490, past fp64 as well
+    (torch.bfloat16, 1, 60, 13440, 16, 1920, 1.8),  # of 464 tokens: 1.8^464 = 3e118
+    (torch.bfloat16, 1, 60, 13440, 32, 1920, 1.8),  # of 15 chunks: 1.8^1920 = 1e490, past fp64 as well
     (torch.float32, 1, 600, 600, 16, 320, 1.4),     # of 320 tokens: 1.4^320 = 6e46
 ])
 def test_prefill_segments_whose_decays_product_passes_fp32(stq, kind, B, H, T, d, grow, rate):
@@ -488,3 +489,13 @@ def test_prompts_keep_the_streams_order(stq, kind, T, captured):
     assert status.item() == 0 and lens.min() < T  # the lengths hang on the outputs before
     for got, w in zip(tensors, want):
         assert torch.equal(got, w)
+
+
+@pytest.mark.parametrize("H,d,T", [(1, 128, 87), (1, 128, 88), (30, 128, 55), (30, 128, 56), (60, 128, 31), (60, 128, 32),
+                                   (3, 64, 63), (3, 64, 64), (3, 32, 79), (3, 32, 80), (300, 32, 127), (300, 32, 128),
+                                   (600, 32, 255), (600, 32, 256), (3, 16, 127), (3, 16, 128), (3, 16, 256), (3, 16, 257),
+                                   (3, 16, 1500), (150, 16, 200), (1, 16, 24575), (1, 16, 24576)])
+@pytest.mark.parametrize("ws", [True, False])
+def test_prefill_forms_meet(stq, H, d, T, ws):
+    """On both sides of the lengths at which bf16 prompts go by chunks, for few heads and many."""
+    check(stq, 1, H, T, d, torch.bfloat16, half=100.0, seed=71, ws=ws)
