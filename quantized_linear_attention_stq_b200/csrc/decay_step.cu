@@ -128,9 +128,12 @@ template <int D, int CW>
 struct SerialCfg {
     static constexpr int SL = D >= 32 ? 8 : 4;                     // lanes sharing a column
     static constexpr int RW = D / SL;                              // rows of a thread
-    static constexpr int CB = CW == 1 ? (D == 32 ? 32 : 16) : (D < 64 ? D : 64);  // columns of a CTA
+    // Columns of a CTA. One column to a thread: few heads are spread over more SMs by 16 than by 32, and as many CTAs
+    // fill the GPU (d = 32, 77 tokens: 15 heads 5.5 and 7.2 us, 148 heads 7.2 and 7.4, 190 heads 9.4 and 11.5).
+    static constexpr int CB = CW == 1 ? 16 : D < 64 ? D : 64;
     static constexpr int NT = CB / CW * SL;
-    static constexpr int TB = CW == 4 ? 16 : D == 32 ? 28 : D == 128 ? 16 : 32;  // tokens staged at a time
+    // Tokens staged at a time, by what 48 KB of shared memory hold of q, k and (one column to a thread) o's parts
+    static constexpr int TB = CW == 4 || D == 128 ? 16 : 32;
 };
 
 template <int D, int IN_BF16, int SUMS, int CW>
@@ -369,8 +372,9 @@ cudaError_t serial(const DecayParams &p, int in_bf16, bool sums, cudaStream_t s)
 }
 
 // Four columns to a thread feed the FMAs from a quarter of the shared memory's reads, one to a thread
-// makes four times the warps. With four and with one, 77 to 100 tokens: d = 128, 32 heads 23 and 17 us, 64 heads
-// 23 and 31; d = 64, 64 heads 15 and 11, 128 heads 19 and 23; d = 32, 160 heads 15.6 and 14.5, 320 heads 19 and 21.
+// makes four times the warps. With four and with one, 100 tokens: d = 128, 40 heads 28.4 and 29.6 us, 64 heads 28.4
+// and 38.7; d = 64, 80 heads 18.9 and 17.8, 128 heads 19.0 and 23.1; d = 32, 200 heads 15.5 and 11.8, 256 heads 15.6
+// and 14.9, 400 heads 18.7 and 22.1.
 bool serial_wide(const DecayParams &p, int d)
 {
     return (int64_t)p.B * p.H * p.segments * d > 50 * 128;
@@ -399,9 +403,9 @@ constexpr int kMostSegments = 1024;  // the join goes along them
 //     latency of a token is all there is: 1 to 16 heads 10 / 13 (64 tokens), 14.0 / 13.1 (96); 32 heads 11.5 / 13.0
 //     (48), 14.4 / 13.0 (64).
 //   d = 64, from 64 on: 1 head 6.8 / 7.6, 64 heads 8.8 / 8.1, 512 heads 30.0 / 30.2.
-//   d = 32, from 80 on: 1 head 8.6 / 6.9, 148 heads 8.8 / 8.2, 256 heads 16.1 / 14.9 (96); 512 heads 24.9 / 28.3
-//     (127), 41 / 39 (192); 1024 heads 34.6 / 49.7 (128), 66 / 70 (256), 98 / 94 (384).
-//   d = 16: an entry's share of a chunk is four times that of d = 64, so token by token, 1024 heads 115 / 190 (1024
+//   d = 32, from 104 on: 1 head 6.5 / 7.0 (96), 8.2 / 7.1 (127), 256 heads 13.8 / 14.8 and 17.7 / 15.0; 400 heads 22
+//     / 22 (112), 35 / 30 (192); 512 heads 36 / 38 (192), 47 / 39 (256); 1024 heads 66 / 70 (256), 98 / 94 (384).
+//   d = 16: a chunk takes nearly d = 64's time for a sixteenth of its state, so token by token, 1024 heads 115 / 190 (1024
 //     tokens), 110 heads 150 / 194 (8192), 16 heads 182 / 266 (65536); but 1 to 148 heads 9.1 / 6.7 (128) and
 //     9.8 / 9.4 (256), and 1 head 50 / 36 (32768), 91 / 49 (65536). Without a cut a token takes 0.05 us, a chunk 2.7,
 //     with up to two rounds of heads; 512 heads 85 / 106 (1024).
@@ -412,7 +416,7 @@ bool by_chunks(int64_t tiles, int T, int d, int in_bf16, bool cut)
         case 16:
             if (!cut) return T >= 128 && tiles <= 2 * kSMs;
             return (T >= 128 && T <= 256 && tiles <= kSMs) || (T >= 24576 && tiles <= 2);
-        case 32: return T >= (tiles <= 256 ? 80 : tiles <= 512 ? 128 : 256);
+        case 32: return T >= (tiles <= 256 ? 104 : tiles <= 448 ? 128 : 224);
         case 64: return T >= 64;
         default: return T >= (tiles < 24 ? 88 : tiles < 48 ? 56 : 32);
     }

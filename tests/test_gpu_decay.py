@@ -492,8 +492,8 @@ def test_prompts_keep_the_streams_order(stq, kind, T, captured):
 
 
 @pytest.mark.parametrize("H,d,T", [(1, 128, 87), (1, 128, 88), (30, 128, 55), (30, 128, 56), (60, 128, 31), (60, 128, 32),
-                                   (3, 64, 63), (3, 64, 64), (3, 32, 79), (3, 32, 80), (300, 32, 127), (300, 32, 128),
-                                   (600, 32, 255), (600, 32, 256), (3, 16, 127), (3, 16, 128), (3, 16, 256), (3, 16, 257),
+                                   (3, 64, 63), (3, 64, 64), (3, 32, 103), (3, 32, 104), (300, 32, 127), (300, 32, 128),
+                                   (600, 32, 223), (600, 32, 224), (3, 16, 127), (3, 16, 128), (3, 16, 256), (3, 16, 257),
                                    (3, 16, 1500), (150, 16, 200), (1, 16, 24575), (1, 16, 24576)])
 @pytest.mark.parametrize("ws", [True, False])
 def test_prefill_forms_meet(stq, H, d, T, ws):
