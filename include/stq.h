@@ -290,7 +290,8 @@ stq_status stq_row_impact(int32_t T, int32_t H, int32_t d, int32_t gate, int32_t
  *   slots       device int32 [B], the pool slot of each request (distinct); a request whose slot is
  *               out of range is skipped and flagged
  *   q, k, v     device [B][H][d] of in_dtype, 16-byte aligned
- *   alpha       device fp32 [B][H], the token's decay of each head (any finite value; 0 clears)
+ *   alpha       device fp32 [B][H], the token's decay of each head (any finite value; 0 clears a finite state: one
+ *               that is not becomes NaN, as 0 times it is)
  *   o           device fp32 [B][H][d], 16-byte aligned, written
  * d in {16, 32, 64, 128}. A state slot has the layout stq_init_state takes and stq_dequantize gives
  * (fp32 [H][d][d]), so an idle request's state can be parked as codes. B == 0 is a no-op. */

@@ -13,23 +13,26 @@
 // memory. S itself stays in registers in fp32 (its sum with b_C S is an ordinary fma; only dS is summed
 // by the tensor cores). Decays are multiplied up, never divided: D_ts is the product of the decays from
 // the end of s's group of 16 tokens, of whole groups and up to t in t's group, so a decay of zero or a
-// product that underflows is as exact as any other. These partial products are made in fp64 and
-// rounded once (an error of theirs would repeat in every chunk of a constant decay).
+// product that underflows is as exact as any other. These partial products, b, e and the chunk's whole product
+// are made in fp64 and rounded once (an error of theirs would repeat in every chunk of a constant decay). D_ts
+// is multiplied from the partial ones in fp32, rounded seven times at most; inside a group of 16 it is a running
+// fp32 product, rounded 14 times at most. Neither error goes into the state.
 //
 // Roles: warps 0-7 turn scores into P, add b O and P V and write o (two warps to each 32 rows, on
 // alternate groups of 16 columns of P and halves of O's columns); warps 8-15 keep S and write its terms;
 // warps 16-23 make e K, 16 tokens at a time, four warps to a group of tokens (for sums only, warps 0-7 do,
-// too; with all 24 the state's warps came late to dS: 458 us instead of 437 for 16 heads of 65521 tokens); warp 24 issues the TMA loads, warp 25 the MMAs, warp 26
+// too; with all 24 the state's warps came late to dS, 5 % of the time of 16 heads of 65521 tokens); warp 24 issues the TMA loads, warp 25 the MMAs, warp 26
 // makes the products of the decays. Products are issued as scores, dS, O, P V: P is made while dS and O
 // run, dS is read while O does (P V then takes its columns of Tensor Memory), S's terms for the next
 // chunk are made from the end of O on, o is read while the next scores run. Roles meet at mbarriers only,
 // each waited for with a limit; a barrier's next phase needs its waiter's progress, so no wait can miss
 // its phase.
 //
-// Bound by the power limit: 16 x 16 heads of 8192 tokens of d = 128 take 650 us in 20 passes, 750 in a
-// second of them, at 1.6 GHz; their tensor work alone would take 415 and 496 us at cuBLAS's rates, their
-// bytes 415. A chunk takes 8200 cycles, 6500 of them of the tensor pipe. 16 heads of 65521 tokens, in nine
-// segments: 420 us, of which the main pass takes 289, the first 104 and the join 7 (floor 206 us of bytes).
+// Bound by the power limit: 16 x 16 heads of 8192 tokens of d = 128 take 770 to 800 us in a second's run, at
+// 1.6 GHz, and 650 to 670 in 20 passes; their tensor work alone would take 496 and 415 us at cuBLAS's rates, their
+// bytes 415. A chunk takes 8140 cycles, and the tensor pipe is active for 5120 of them (counters of that case). 16
+// heads of 65521 tokens, in nine segments: 475 to 515 us in a second's run, 420 in 20 passes, of which the main pass
+// takes 289, the first 104 and the join 7 (floor 206 us of bytes).
 //
 // A group of 16 scores (16 fp32 columns of Tensor Memory) is replaced in place by the h and m terms of
 // its 16 entries of P (8 columns each); the l terms have columns of their own.
