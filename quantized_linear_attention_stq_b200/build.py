@@ -68,13 +68,13 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
         import torch
     except ImportError:
         torch = None
+    if torch is not None and not force and not binding_stale():
+        return BINDING
     cxx, python_h = shutil.which("g++"), os.path.join(sysconfig.get_paths()["include"], "Python.h")
     missing = "torch" if torch is None else "g++" if cxx is None else "" if os.path.exists(python_h) else python_h
     if missing:
         warnings.warn(f"_binding.so is not built: {missing} is missing")
         return ""
-    if not force and not binding_stale():
-        return BINDING
     src, key = os.path.join(CSRC, "binding.cpp"), binding_key()
     root = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")

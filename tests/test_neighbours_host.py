@@ -265,6 +265,8 @@ def test_library_is_built_without_the_bindings_tools(stq, monkeypatch, what):
         monkeypatch.setattr(build.shutil, "which", lambda name: None if name == "g++" else which(name))
     else:
         monkeypatch.setattr(build.sysconfig, "get_paths", lambda: {"include": "/nowhere"})
+    assert build.build_binding() == build.BINDING  # nothing is missing for one that is up to date
+    monkeypatch.setattr(build, "binding_stale", lambda: True)
     with pytest.warns(UserWarning, match="not built"):
         assert build.build() == build.LIB
     with pytest.warns(UserWarning, match="not built"):
