@@ -305,7 +305,8 @@ size_t stq_decay_prefill_workspace_bytes(int32_t B, int32_t H, int32_t T, int32_
 
 /* The same recurrence over prompts: token t of request b is the decay step on (q, k, v, alpha) at t.
  *   q, k, v     device [B][H][T][d] of in_dtype, 16-byte aligned
- *   alpha       device fp32 [B][H][T]; products of up to 128 decays in a row have to stay finite
+ *   alpha       device fp32 [B][H][T]; products of up to 128 decays in a row have to stay finite (one below
+ *               2^-126 loses digits)
  *   lens        device int32 [B], tokens of each prompt, or NULL: T for all. Tokens behind a prompt's
  *               end change nothing: their rows of q, k, v and alpha are not used (NaN may stand
  *               there) and their rows of o stay as they were. A length outside [0, T] skips the
@@ -370,13 +371,15 @@ size_t stq_paged_attention_workspace_bytes(int32_t B, int32_t q_heads, int32_t d
  *   table       device int32 [B][table_width]; entries behind a request's last page are not read
  *   lens        device int32 [B], cached tokens (the new one included). 0 (a padded row) gives o = 0;
  *               a length outside [0, table_width * page_size] does too, and is flagged
- *   scale       finite
+ *   scale       finite, and so log2(e) times it
  *   o           device fp32 [B][q_heads][d], 16-byte aligned, written
  *   workspace   device scratch of >= stq_paged_attention_workspace_bytes(...) bytes, 256-byte
  *               aligned, or NULL. With it the cached tokens of all requests are split evenly over
  *               the GPU and the parts joined; without it one thread block reads a key-value head's
  *               whole cache (slower for few or long requests). Given but too small or misaligned:
  *               STQ_ERR_INVALID_ARG. Calls in flight at the same time need separate workspaces.
+ * A cached value or score that is not finite makes its outputs infinite or NaN, and is flagged; a score of -inf
+ * only drops its token.
  * Rows of a page behind a request's last token are not used (NaN may stand there). Tokens on a page
  * outside [0, num_pages) are left out and flagged. A row whose scores are all -inf gives o = 0.
  * d in {16, 32, 64, 128}. B == 0 is a no-op. */

@@ -842,8 +842,10 @@ extern "C" stq_status stq_paged_attention(int32_t B, int32_t q_heads, int32_t kv
                                           size_t workspace_bytes, int32_t *dev_status, void *stream)
 {
     if (B < 0 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads != 0 || page_size < 1 || num_pages < 0 ||
-        table_width < 0 || (dtype != STQ_F32 && dtype != STQ_BF16) || !(scale - scale == 0.f))
+        table_width < 0 || (dtype != STQ_F32 && dtype != STQ_BF16))
         return STQ_ERR_INVALID_ARG;
+    const float scale2 = scale * 1.4426950408889634f;
+    if (!(scale2 - scale2 == 0.f)) return STQ_ERR_INVALID_ARG;
     if (!(d == 16 || d == 32 || d == 64 || d == 128)) return STQ_ERR_UNSUPPORTED;
     if (B == 0) return STQ_OK;
     if (!q || !lens || !o || (table_width > 0 && (!table || !k_pages || !v_pages))) return STQ_ERR_INVALID_ARG;
@@ -868,7 +870,7 @@ extern "C" stq_status stq_paged_attention(int32_t B, int32_t q_heads, int32_t kv
     p.lens = lens;
     p.o = o;
     p.status = dev_status;
-    p.scale2 = scale * 1.4426950408889634f;
+    p.scale2 = scale2;
     p.B = B;
     p.Hq = q_heads;
     p.Hkv = kv_heads;

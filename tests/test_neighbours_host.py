@@ -280,3 +280,11 @@ def test_workspace_of_another_kind_is_named(stq):
         stq.paged_attention(z(2, 4, 16), z(3, 2, 8, 16), z(3, 2, 8, 16), z(2, 5, t=i), z(2, t=i), z(2, 4, 16), 1.0, workspace="x")
     with pytest.raises(TypeError, match="workspace"):
         stq.decay_prefill(z(1, 1, 16, 16), z(1, t=i), *[z(1, 1, 2000, 16)] * 3, z(1, 1, 2000), z(1, 1, 2000, 16), workspace=b"x")
+
+
+def test_attention_refuses_a_scale_that_overflows(stq):
+    """Scores are taken in base 2: log2(e) times the scale has to be finite too."""
+    L = stq.lib()
+    for scale in (2.4e38, -3.4e38):
+        assert attend(L, scale=scale) == INVALID
+    assert attend(L, scale=2.3e38, d=256) == UNSUPPORTED  # the next check
