@@ -499,3 +499,10 @@ def test_prompts_keep_the_streams_order(stq, kind, T, captured):
 def test_prefill_forms_meet(stq, H, d, T, ws):
     """On both sides of the lengths at which bf16 prompts go by chunks, for few heads and many."""
     check(stq, 1, H, T, d, torch.bfloat16, half=100.0, seed=71, ws=ws)
+
+
+@pytest.mark.parametrize("kind,T,d", [(torch.float32, 1, 32), (torch.float32, 3, 16), (torch.bfloat16, 40, 16), (torch.bfloat16, 130, 16)])
+def test_more_heads_than_a_grid_dimension(stq, kind, T, d):
+    """More (request, head) pairs than 32768, with requests of several lengths among them."""
+    B, H = 11, 3001
+    check(stq, B, H, T, d, kind, step=T == 1, lens=None if T == 1 else [T, 0, 1] + [T] * 7 + [T - 1], seed=81)
