@@ -341,8 +341,8 @@ stq_status stq_decay_prefill(int32_t B, int32_t H, int32_t T, int32_t d, int32_t
  *   lens_out    device int32 [B], written: lens + fresh;  may be lens itself
  *   head_out    device int32 [1], written: the list's new head;  may be free_head itself
  * All or nothing per request: one with a negative count, with more tokens than its table row spans or
- * than int32 counts, for whose pages the list (taken in order) is too short, or whose tokens pass the slot map's end gets no
- * pages; its length and table row stay, its tokens' slots are -1, and STQ_ERR_BOUNDS is flagged. A
+ * than int32 counts, for whose pages the list (taken in order) is too short, or whose tokens pass the
+ * slot map's end gets no pages; its length and table row stay, its tokens' slots are -1, and STQ_ERR_BOUNDS is flagged. A
  * request that needs no new page is served whatever the list holds. Slots must be int32: a page
  * whose slots are not (or a negative page) gives -1 and is flagged. */
 stq_status stq_page_plan(int32_t B, int32_t table_width, int32_t page_size, int32_t *table, const int32_t *lens,

@@ -28,7 +28,7 @@
 // each waited for with a limit; a barrier's next phase needs its waiter's progress, so no wait can miss
 // its phase.
 //
-// Bound by the power limit: 16 x 16 heads of 8192 tokens of d = 128 take 770 to 800 us in a second's run, at
+// Bound by the power limit: 16 x 16 heads of 8192 tokens of d = 128 take 760 to 800 us in a second's run, at
 // 1.6 GHz, and 650 to 670 in 20 passes; their tensor work alone would take 496 and 415 us at cuBLAS's rates, their
 // bytes 415. A chunk takes 8140 cycles, and the tensor pipe is active for 5120 of them (counters of that case). 16
 // heads of 65521 tokens, in nine segments: 475 to 515 us in a second's run, 420 in 20 passes, of which the main pass

@@ -8,7 +8,7 @@
 // its store, all loads of a thread in flight at once; a warp's lanes hold consecutive columns, so
 // rows move in whole 128-byte lines and the readout is a sum over the CTA's row groups.
 //
-// Token by token (fp32 inputs, short prompts). The state of a block of columns stays in registers for the
+// Token by token (fp32 inputs, most bf16 ones of d = 16, short prompts). The state of a block of columns stays in registers for the
 // whole prompt (columns of S are independent of each other); tokens are staged through shared memory 16 or
 // 32 at a time. A column's rows are spread over SL lanes, joined by shuffles per token. Bound by the FMAs,
 // three to an entry and token (32 heads of 2048 tokens of d = 128: 269 us, of which 89 at the FMAs' rate).
